@@ -143,6 +143,88 @@ int dsa_sparse_mla_attn_paged(const void* q, const void* kv_pages, int num_pages
                               int k, float scale, void* out, float* lse, void* stream);
 
 /*
+ * Dense MLA attention in MQA mode of new tokens over the paged latent cache
+ * (the form without an index set: contexts of up to k tokens, layers without
+ * an indexer, checking drafted tokens). seq, pos, block_table and kv_pages as
+ * dsa_sparse_mla_attn_paged. With S = max_pages * page_size, row t sees
+ *   window = 0   the keys s <= min(pos[t], S - 1) of sequence seq[t];
+ *   window > 0   of those, s > pos[t] - window (the last `window`, its own
+ *                among them) and s < sinks (the first tokens stay visible).
+ *   q    bf16 [T, Hq, d_qk]
+ *   out  bf16 [T, Hq, d_v] (out)   sum_s softmax_s(scale q.c_s) c_s[0:d_v]
+ *   lse  fp32 [T, Hq] (out)        log sum_s exp(scale q.c_s)
+ * A row that sees no key (seq outside [0, n_seqs), pos < 0: a padded batch)
+ * gets out = 0 and lse = -inf. Keys that a row does not see take no part in
+ * it, whatever the pool holds there (NaN among it). Consecutive rows of one
+ * sequence may be any tokens of it, in any order; those of a chunk are
+ * cheapest next to each other. Probabilities are rounded to bf16 for the
+ * product with the values; logits, maxima and sums are fp32.
+ * Supported: 1 <= Hq <= 128, d_qk = 576, d_v = 512, T * Hq < 2^31, sinks > 0
+ * only with a window. workspace: dsa_mla_attn_paged_workspace_size(T, Hq)
+ * bytes; calls in flight at once, captured graphs among them, need one each.
+ */
+size_t dsa_mla_attn_paged_workspace_size(int T, int Hq);
+int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
+                       const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
+                       const int32_t* pos, int T, int Hq, int d_qk, int d_v, float scale, int window, int sinks,
+                       void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The attention weight that each cached token receives from those rows:
+ *   mass[b, s] += sum over the rows t of sequence b that see s, and the heads
+ *                 h, of exp(scale q[t,h].c_s - lse[t,h])
+ *   lse   fp32 [T, Hq]   dsa_mla_attn_paged's for the same rows and window
+ *                        (a row's -inf adds nothing)
+ *   mass  fp32 [n_seqs, max_pages * page_size]   ACCUMULATED into; positions
+ *                        that no row sees keep their value
+ * Every element is added to by one thread, in the order of the rows: results
+ * do not vary from run to run. Other arguments and limits as
+ * dsa_mla_attn_paged; no workspace. Asynchronous on `stream`.
+ */
+int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
+                            const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
+                            const int32_t* pos, const float* lse, int T, int Hq, int d_qk, float scale, int window,
+                            int sinks, float* mass, void* stream);
+
+/*
+ * Eviction from a cache by accumulated weight, first half: which positions
+ * stay. With n = seq_len[b] (taken into [0, max_len]): all of them for
+ * n <= keep; else the first `sinks`, the last `recent`, and of the others the
+ * keep - sinks - recent with the largest mass (ties to the lower position, a
+ * NaN ranks with -inf).
+ *   mass      fp32 [n_seqs, max_len]
+ *   seq_len   int32 [n_seqs]
+ *   keep_idx  int32 [n_seqs, keep] (out)  the positions, ascending, then -1
+ *   new_len   int32 [n_seqs] (out)        min(n, keep)
+ * Supported: keep >= 1, sinks + recent <= keep, max_len <= 2^30. No
+ * workspace. Asynchronous on `stream`.
+ */
+int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_len, int n_seqs, int keep, int sinks,
+                           int recent, int32_t* keep_idx, int32_t* new_len, void* stream);
+
+/*
+ * Second half: the kept rows move, in place, to the front of their sequence:
+ * for j < new_len[b] the cache row of position keep_idx[b, j] becomes that of
+ * position j, in the latent pages and, where given, in the indexer's key
+ * pages (k_pages, NULL: none) and in mass (NULL: none), whose places from
+ * new_len[b] on become 0. All other rows stay as they are; the pages behind
+ * ceil(new_len / page_size) are then free. Rotary parts keep the angle of the
+ * token's first position: positions name cache places from here on.
+ *   kv_pages  [num_pages * page_size] rows of kv_row_bytes bytes
+ *   k_pages   [num_pages * page_size] rows of k_row_bytes bytes, or NULL
+ *   keep_idx  as dsa_cache_evict_select writes it: ascending, keep_idx[b, j]
+ *             >= j. A row whose entry is below j or beyond the table, or one
+ *             of whose pages lies outside the pool, is not moved.
+ *   mass      fp32 [n_seqs, max_pages * page_size] or NULL
+ * A page may stand in the table once only (a shared prefix has to be copied
+ * first). Supported: row bytes multiples of 16 up to 4096. No workspace.
+ * Asynchronous on `stream`.
+ */
+int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int k_row_bytes, int num_pages,
+                            int page_size, const int32_t* block_table, int n_seqs, int max_pages,
+                            const int32_t* keep_idx, int keep, const int32_t* new_len, float* mass, void* stream);
+
+/*
  * Sparse MQA attention over the selected latent rows ("Attention" and "DSA
  * under MLA (MQA Mode)", section 2 of "Paper Breakdown: DeepSeek-V3.2").
  *

@@ -11,6 +11,11 @@ Entry points mirror the C ABI:
   * ``indexer_topk``     lightning indexer + Top-k selector -> idx [T, k]
   * ``sparse_mla_attn``  sparse MQA attention over idx -> out [T, Hq, d_v], lse [T, Hq]
   * ``forward``          both, on one stream
+  * ``mla_attn_paged``   dense MLA attention of new tokens over the paged latent
+    cache, or its last ``window`` and first ``sinks`` tokens -> out, lse
+  * ``mla_attn_mass_paged``, ``cache_evict_select``, ``cache_compact_paged``
+    the weight each cached token receives, which tokens stay, and the move of
+    both caches' rows
   * ``workspace_size``, ``device_status``, ``last_error``
 """
 from __future__ import annotations
@@ -38,7 +43,9 @@ EXPORTS = ("dsa_workspace_size", "dsa_indexer_topk", "dsa_sparse_mla_attn", "dsa
            "dsa_sparse_mla_attn_bwd_workspace_size", "dsa_indexer_kl", "dsa_indexer_kl_workspace_size",
            "dsa_mla_mha_attn", "dsa_partition_prefill_rows", "dsa_partition_decode_seqs",
            "dsa_sparse_mla_attn_split", "dsa_sparse_mla_attn_split_workspace_size", "dsa_debug_build",
-           "dsa_debug_counters", "dsa_phase_timing", "dsa_phase_times")
+           "dsa_debug_counters", "dsa_phase_timing", "dsa_phase_times", "dsa_mla_attn_paged",
+           "dsa_mla_attn_paged_workspace_size", "dsa_mla_attn_mass_paged", "dsa_cache_evict_select",
+           "dsa_cache_compact_paged")
 
 
 class DSAError(RuntimeError):
@@ -96,6 +103,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dsa_indexer_kl.restype = I
         lib.dsa_mla_mha_attn.argtypes = [P, P, P, I, I, I, I, I, F, P, P, P]
         lib.dsa_mla_mha_attn.restype = I
+        lib.dsa_mla_attn_paged_workspace_size.argtypes = [I, I]
+        lib.dsa_mla_attn_paged_workspace_size.restype = Z
+        lib.dsa_mla_attn_paged.argtypes = [P, P, I, I, P, I, I, P, P, I, I, I, I, F, I, I, P, P, P, Z, P]
+        lib.dsa_mla_attn_paged.restype = I
+        lib.dsa_mla_attn_mass_paged.argtypes = [P, P, I, I, P, I, I, P, P, P, I, I, I, F, I, I, P, P]
+        lib.dsa_mla_attn_mass_paged.restype = I
+        lib.dsa_cache_evict_select.argtypes = [P, I, P, I, I, I, I, P, P, P]
+        lib.dsa_cache_evict_select.restype = I
+        lib.dsa_cache_compact_paged.argtypes = [P, I, P, I, I, I, P, I, I, P, I, P, P, P]
+        lib.dsa_cache_compact_paged.restype = I
         lib.dsa_partition_prefill_rows.argtypes = [I] * 9 + [P]
         lib.dsa_partition_prefill_rows.restype = I
         lib.dsa_partition_decode_seqs.argtypes = [P, I, I, I, I, I, P]
@@ -337,6 +354,173 @@ def sparse_mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, id
         _ptr(pos), _ptr(idx), T, Hq, d_qk, d_v, k, float(scale), _ptr(out), _ptr(lse),
         _stream(stream)))
     return out, lse
+
+
+class _Launch:
+    """The device and stream of one call: the operands' device is made current
+    (a stream belongs to one), and `stream` defaults to its current stream.
+    Buffers that the call itself allocates are kept from reuse until a
+    caller's other stream is done with them."""
+
+    def __init__(self, device, stream):
+        self.device, self.given = device, stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.device.index is not None and self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def keep(self, t):
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+    @property
+    def handle(self):
+        return _stream(self.given)
+
+
+def _pages(t, name, cols=None, dtype=None, page_size=0, device=None):
+    """Checked page pool [num_pages * page_size, cols]: (tensor, num_pages)."""
+    t = _dev(t, name, device)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [rows, {cols or 'columns'}], got shape {tuple(t.shape)}")
+    if page_size <= 0 or t.shape[0] % page_size:
+        raise ValueError(f"{name} has {t.shape[0]} rows, not a whole number of {page_size}-row pages")
+    return t, t.shape[0] // page_size
+
+
+def _cache_rows(q, kv_pages, page_size, block_table, seq, pos):
+    """Checked operands of attention over the paged latent cache:
+    (q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, device)."""
+    q = _dev(q, "q")
+    if q.dtype != torch.bfloat16 or q.dim() != 3:
+        raise TypeError(f"q must be bfloat16 [T, Hq, d_qk], got {q.dtype} {tuple(q.shape)}")
+    T, Hq, d_qk = q.shape
+    dev = q.device
+    kv_pages, num_pages = _pages(kv_pages, "kv_pages", d_qk, torch.bfloat16, page_size, dev)
+    block_table, seq, pos = _paged_tables(block_table, seq, pos, T, dev)
+    return q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev
+
+
+def alloc_mla_attn_workspace(T: int, Hq: int, device=None) -> torch.Tensor:
+    """Workspace of ``mla_attn_paged`` for T rows of Hq heads."""
+    n = int(load_library().dsa_mla_attn_paged_workspace_size(T, Hq))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: float, d_v: int, window: int = 0,
+                   sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """(out bf16 [T, Hq, d_v], lse fp32 [T, Hq]) of dense MQA-mode attention of T
+    new tokens over a paged latent cache: row t sees the keys s <= pos[t] of
+    sequence seq[t], and with window > 0 only the last `window` of them and
+    the first `sinks`. A row without keys gives out = 0, lse = -inf."""
+    q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
+                                                                                  block_table, seq, pos)
+    with _Launch(dev, stream) as at:
+        if out is None:
+            out = at.keep(torch.empty((T, Hq, d_v), dtype=torch.bfloat16, device=dev))
+        if lse is None:
+            lse = at.keep(torch.empty((T, Hq), dtype=torch.float32, device=dev))
+        if workspace is None:
+            workspace = at.keep(alloc_mla_attn_workspace(T, Hq, dev))
+        out = _arg(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
+        lse = _arg(lse, "lse", torch.float32, (T, Hq), dev)
+        nbytes = _ws(workspace, dev)
+        _check(load_library().dsa_mla_attn_paged(
+            _ptr(q), _ptr(kv_pages), num_pages, page_size, _ptr(block_table), block_table.shape[0],
+            block_table.shape[1], _ptr(seq), _ptr(pos), T, Hq, d_qk, d_v, float(scale), int(window), int(sinks),
+            _ptr(out), _ptr(lse), _ptr(workspace), nbytes, at.handle))
+    return out, lse
+
+
+def mla_attn_mass_paged(q, kv_pages, page_size: int, block_table, seq, pos, lse, scale: float, mass=None,
+                        window: int = 0, sinks: int = 0, stream=None):
+    """mass fp32 [n_seqs, max_pages * page_size] += the attention weight (over
+    rows and heads) that each cached token receives from these rows.
+
+    lse is ``mla_attn_paged``'s for the same rows, window and sinks. mass is
+    accumulated into (a new zeroed tensor when None)."""
+    q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
+                                                                                  block_table, seq, pos)
+    lse = _arg(lse, "lse", torch.float32, (T, Hq), dev)
+    shape = (block_table.shape[0], block_table.shape[1] * page_size)
+    with _Launch(dev, stream) as at:
+        if mass is None:
+            with torch.cuda.stream(at.given):
+                mass = at.keep(torch.zeros(shape, dtype=torch.float32, device=dev))
+        mass = _arg(mass, "mass", torch.float32, shape, dev)
+        _check(load_library().dsa_mla_attn_mass_paged(
+            _ptr(q), _ptr(kv_pages), num_pages, page_size, _ptr(block_table), shape[0], block_table.shape[1],
+            _ptr(seq), _ptr(pos), _ptr(lse), T, Hq, d_qk, float(scale), int(window), int(sinks), _ptr(mass),
+            at.handle))
+    return mass
+
+
+def cache_evict_select(mass, seq_len, keep: int, sinks: int = 0, recent: int = 0, keep_idx=None, new_len=None,
+                       stream=None):
+    """(keep_idx int32 [n_seqs, keep], new_len int32 [n_seqs]): the positions of
+    each sequence that stay when at most `keep` may: the first `sinks`, the
+    last `recent` and the others with the largest mass [n_seqs, max_len],
+    ascending and -1 padded."""
+    mass = _dev(mass, "mass")
+    dev = mass.device
+    if mass.dtype != torch.float32 or mass.dim() != 2:
+        raise TypeError(f"mass must be float32 [n_seqs, max_len], got {mass.dtype} {tuple(mass.shape)}")
+    n_seqs, max_len = mass.shape
+    seq_len = _i32(seq_len, "seq_len", (n_seqs,), dev)
+    if keep <= 0:
+        raise ValueError(f"keep = {keep} must be positive")
+    with _Launch(dev, stream) as at:
+        if keep_idx is None:
+            keep_idx = at.keep(torch.empty((n_seqs, keep), dtype=torch.int32, device=dev))
+        if new_len is None:
+            new_len = at.keep(torch.empty(n_seqs, dtype=torch.int32, device=dev))
+        keep_idx = _arg(keep_idx, "keep_idx", torch.int32, (n_seqs, keep), dev)
+        new_len = _arg(new_len, "new_len", torch.int32, (n_seqs,), dev)
+        _check(load_library().dsa_cache_evict_select(_ptr(mass), max_len, _ptr(seq_len), n_seqs, int(keep),
+                                                     int(sinks), int(recent), _ptr(keep_idx), _ptr(new_len),
+                                                     at.handle))
+    return keep_idx, new_len
+
+
+def cache_compact_paged(kv_pages, page_size: int, block_table, keep_idx, new_len, k_pages=None, mass=None,
+                        stream=None) -> None:
+    """Move the kept rows of each sequence, in place, to its positions 0 ..
+    new_len - 1: in kv_pages, and where given in k_pages (the indexer's keys,
+    same pages) and mass [n_seqs, max_pages * page_size], which becomes 0
+    behind them. keep_idx and new_len are ``cache_evict_select``'s."""
+    kv_pages, num_pages = _pages(kv_pages, "kv_pages", page_size=page_size)
+    dev = kv_pages.device
+    block_table = _dev(block_table, "block_table", dev)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise TypeError("block_table must be int32 [n_seqs, max_pages]")
+    n_seqs, max_pages = block_table.shape
+    keep_idx = _dev(keep_idx, "keep_idx", dev)
+    if keep_idx.dtype != torch.int32 or keep_idx.dim() != 2 or keep_idx.shape[0] != n_seqs:
+        raise TypeError(f"keep_idx must be int32 [{n_seqs}, keep], got {keep_idx.dtype} {tuple(keep_idx.shape)}")
+    new_len = _i32(new_len, "new_len", (n_seqs,), dev)
+    k_bytes = 0
+    if k_pages is not None:
+        k_pages, k_num = _pages(k_pages, "k_pages", page_size=page_size, device=dev)
+        if k_num != num_pages:
+            raise ValueError(f"k_pages has {k_num} pages, kv_pages {num_pages}")
+        k_bytes = k_pages.shape[1] * k_pages.element_size()
+    if mass is not None:
+        mass = _arg(mass, "mass", torch.float32, (n_seqs, max_pages * page_size), dev)
+    with _Launch(dev, stream) as at:
+        _check(load_library().dsa_cache_compact_paged(
+            _ptr(kv_pages), kv_pages.shape[1] * kv_pages.element_size(), _ptr(k_pages), k_bytes, num_pages,
+            page_size, _ptr(block_table), n_seqs, max_pages, _ptr(keep_idx), keep_idx.shape[1], _ptr(new_len),
+            _ptr(mass), at.handle))
 
 
 def sparse_mla_attn(q, kv, idx, scale: float, d_v: int, pos=None, k_base=None, out=None,

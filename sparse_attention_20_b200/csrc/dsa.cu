@@ -19,6 +19,8 @@
 #include "mha_tc.cuh"
 #include "attn_simple.cuh"
 #include "attn_tc.cuh"
+#include "cache_attn.cuh"
+#include "cache_evict.cuh"
 #include "common.cuh"
 #include "debug_checks.cuh"
 #include "indexer_chunked.cuh"
@@ -1145,6 +1147,148 @@ int dsa_sparse_mla_attn_paged(const void* q, const void* kv_pages, int num_pages
     if (int rc = debug_check(idx, pos, nullptr, T, S, k, pg, false, st)) return rc;
     return attn_tc(reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(kv_pages),
                    idx, pos, nullptr, T, S, k, scale, reinterpret_cast<__nv_bfloat16*>(out), lse, st, pg);
+}
+
+namespace {
+// Arguments the dense paged attention and the weights' accumulation share.
+int check_cache_attn(const void* q, const void* kv_pages, int num_pages, int page_size, const int32_t* block_table,
+                     int n_seqs, int max_pages, const int32_t* seq, const int32_t* pos, const float* lse, int T,
+                     int Hq, int d_qk, int window, int sinks)
+{
+    if (int rc = check_paged(kv_pages, num_pages, page_size, block_table, n_seqs, max_pages, seq, pos, T))
+        return rc;
+    if (!q || !lse) return fail(DSA_ERR_ARG, "NULL q or lse");
+    if (!al16(q) || !al16(lse)) return fail(DSA_ERR_ARG, "q and lse must be 16-byte aligned");
+    if (Hq <= 0 || Hq > 128) return fail(DSA_ERR_UNSUPPORTED, "Hq=%d (supported: 1..128)", Hq);
+    if ((long long)T * Hq > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T * Hq = %lld", (long long)T * Hq);
+    if (d_qk != dsa::cache_attn::kDqk)
+        return fail(DSA_ERR_UNSUPPORTED, "d_qk=%d (supported: %d)", d_qk, dsa::cache_attn::kDqk);
+    if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
+        return fail(DSA_ERR_ARG, "window=%d, sinks=%d (both >= 0; sinks only with a window)", window, sinks);
+    return DSA_OK;
+}
+
+dsa::PagedRows paged_rows(const int32_t* block_table, const int32_t* seq, int n_seqs, int max_pages, int page_size,
+                          int num_pages)
+{
+    dsa::PagedRows pg;
+    pg.block_table = block_table;
+    pg.seq = seq;
+    pg.n_seqs = n_seqs;
+    pg.max_pages = max_pages;
+    pg.page_size = page_size;
+    pg.num_pages = num_pages;
+    return pg;
+}
+}  // namespace
+
+size_t dsa_mla_attn_paged_workspace_size(int T, int Hq)
+{
+    if (T <= 0 || Hq <= 0) return 0;
+    return 0;
+}
+
+int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
+                       const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
+                       const int32_t* pos, int T, int Hq, int d_qk, int d_v, float scale, int window, int sinks,
+                       void* out, float* lse, void* workspace, size_t ws_bytes, void* stream)
+{
+    using namespace dsa::cache_attn;
+    g_err[0] = 0;
+    if (int rc = check_cache_attn(q, kv_pages, num_pages, page_size, block_table, n_seqs, max_pages, seq, pos, lse,
+                                  T, Hq, d_qk, window, sinks))
+        return rc;
+    if (!out || !al16(out)) return fail(DSA_ERR_ARG, "out must be a 16-byte aligned pointer");
+    if (d_v != kDv) return fail(DSA_ERR_UNSUPPORTED, "d_v=%d (supported: %d)", d_v, kDv);
+    const size_t need = dsa_mla_attn_paged_workspace_size(T, Hq);
+    if (need && (!workspace || ws_bytes < need || !al16(workspace)))
+        return fail(DSA_ERR_WORKSPACE, "paged attention needs %zu workspace bytes (got %zu)", need, ws_bytes);
+    const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
+    const long long rows = (long long)T * Hq;
+    mla_attn_paged_simple_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(kv_pages), pg, pos, T, Hq,
+        scale, window, sinks, reinterpret_cast<__nv_bfloat16*>(out), lse);
+    DSA_LAUNCH_CHECK("mla_attn_paged_simple_kernel");
+    return DSA_OK;
+}
+
+int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
+                            const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
+                            const int32_t* pos, const float* lse, int T, int Hq, int d_qk, float scale, int window,
+                            int sinks, float* mass, void* stream)
+{
+    using namespace dsa::cache_attn;
+    g_err[0] = 0;
+    if (int rc = check_cache_attn(q, kv_pages, num_pages, page_size, block_table, n_seqs, max_pages, seq, pos, lse,
+                                  T, Hq, d_qk, window, sinks))
+        return rc;
+    if (!mass || !al16(mass)) return fail(DSA_ERR_ARG, "mass must be a 16-byte aligned pointer");
+    const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
+    const long long keys = (long long)n_seqs * max_pages * page_size;
+    mla_attn_mass_simple_kernel<<<(unsigned)((keys + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(kv_pages), pg, pos, lse, T,
+        Hq, scale, window, sinks, mass);
+    DSA_LAUNCH_CHECK("mla_attn_mass_simple_kernel");
+    return DSA_OK;
+}
+
+int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_len, int n_seqs, int keep, int sinks,
+                           int recent, int32_t* keep_idx, int32_t* new_len, void* stream)
+{
+    using namespace dsa::cache_evict;
+    g_err[0] = 0;
+    if (!mass || !seq_len || !keep_idx || !new_len)
+        return fail(DSA_ERR_ARG, "NULL mass, seq_len, keep_idx or new_len");
+    if (!al16(mass) || !al16(seq_len) || !al16(keep_idx) || !al16(new_len))
+        return fail(DSA_ERR_ARG, "mass, seq_len, keep_idx and new_len must be 16-byte aligned");
+    if (n_seqs <= 0 || max_len <= 0 || keep <= 0)
+        return fail(DSA_ERR_ARG, "n_seqs=%d, max_len=%d, keep=%d must be positive", n_seqs, max_len, keep);
+    if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
+        return fail(DSA_ERR_ARG, "sinks=%d and recent=%d must be >= 0 and at most keep=%d together", sinks, recent,
+                    keep);
+    if (max_len > kMaxLen) return fail(DSA_ERR_UNSUPPORTED, "max_len=%d (supported: up to %d)", max_len, kMaxLen);
+    cache_evict_select_kernel<<<n_seqs, kSelectThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        mass, max_len, seq_len, max_len, keep, sinks, recent, keep_idx, new_len);
+    DSA_LAUNCH_CHECK("cache_evict_select_kernel");
+    return DSA_OK;
+}
+
+int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int k_row_bytes, int num_pages,
+                            int page_size, const int32_t* block_table, int n_seqs, int max_pages,
+                            const int32_t* keep_idx, int keep, const int32_t* new_len, float* mass, void* stream)
+{
+    using namespace dsa::cache_evict;
+    g_err[0] = 0;
+    if (!kv_pages || !block_table || !keep_idx || !new_len)
+        return fail(DSA_ERR_ARG, "NULL kv_pages, block_table, keep_idx or new_len");
+    if (!al16(kv_pages) || !al16(k_pages) || !al16(block_table) || !al16(keep_idx) || !al16(new_len) || !al16(mass))
+        return fail(DSA_ERR_ARG, "every pointer must be 16-byte aligned");
+    if (num_pages <= 0 || page_size <= 0 || n_seqs <= 0 || max_pages <= 0 || keep <= 0)
+        return fail(DSA_ERR_ARG, "num_pages=%d, page_size=%d, n_seqs=%d, max_pages=%d, keep=%d must be positive",
+                    num_pages, page_size, n_seqs, max_pages, keep);
+    if ((long long)num_pages * page_size > INT32_MAX || (long long)max_pages * page_size > INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "cache of more than 2^31 rows");
+    if (kv_row_bytes <= 0 || kv_row_bytes % 16 || kv_row_bytes > kMaxRowBytes ||
+        (k_pages && (k_row_bytes <= 0 || k_row_bytes % 16 || k_row_bytes > kMaxRowBytes)))
+        return fail(DSA_ERR_UNSUPPORTED, "rows of %d and %d bytes (supported: multiples of 16 up to %d)",
+                    kv_row_bytes, k_row_bytes, kMaxRowBytes);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dsa::PagedRows pg = paged_rows(block_table, nullptr, n_seqs, max_pages, page_size, num_pages);
+    constexpr int slice = 128;
+    cache_compact_kernel<<<dim3(n_seqs, dsa::ceil_div(kv_row_bytes, slice)), kCompactThreads, 0, st>>>(
+        reinterpret_cast<uint8_t*>(kv_pages), kv_row_bytes, slice, pg, keep_idx, keep, new_len);
+    DSA_LAUNCH_CHECK("cache_compact_kernel");
+    if (k_pages) {
+        cache_compact_kernel<<<dim3(n_seqs, dsa::ceil_div(k_row_bytes, slice)), kCompactThreads, 0, st>>>(
+            reinterpret_cast<uint8_t*>(k_pages), k_row_bytes, slice, pg, keep_idx, keep, new_len);
+        DSA_LAUNCH_CHECK("cache_compact_kernel");
+    }
+    if (mass) {
+        cache_compact_mass_kernel<<<n_seqs, kCompactThreads, 0, st>>>(mass, max_pages * page_size, keep_idx, keep,
+                                                                      new_len);
+        DSA_LAUNCH_CHECK("cache_compact_mass_kernel");
+    }
+    return DSA_OK;
 }
 
 int dsa_sparse_mla_attn(const void* q, const void* kv, const int32_t* idx, const int32_t* pos,
