@@ -30,53 +30,6 @@ __device__ __forceinline__ Visible visible_of(int n_keys, int pos, int window, i
     return v;
 }
 
-// One warp per (row, head): a lane holds 18 of the 576 columns.
-__global__ void __launch_bounds__(256)
-mla_attn_paged_simple_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kv,
-                             const PagedRows pg, const int* __restrict__ pos, int T, int Hq, float scale,
-                             int window, int sinks, __nv_bfloat16* __restrict__ out, float* __restrict__ lse)
-{
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)T * Hq) return;
-    const int t = (int)(row / Hq);
-    long long base;
-    const int* bt;
-    const int n = row_keys(pg, pos, nullptr, t, T, 0, &base, &bt);
-    const Visible vis = visible_of(n, n > 0 ? pos[t] : 0, window, sinks);
-    float2 qv[9], acc[8];
-    for (int i = 0; i < 9; ++i)
-        qv[i] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(q + row * kDqk)[i * 32 + lane]);
-    for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    for (int s = 0; s < n; ++s) {
-        if (s >= vis.sink_end && s < vis.lo) s = vis.lo;
-        if (s >= n) break;
-        const __nv_bfloat162* c = reinterpret_cast<const __nv_bfloat162*>(kv + key_row(pg, bt, base, s) * kDqk);
-        float2 cv[9];
-        float x = 0.f;
-        for (int i = 0; i < 9; ++i) {
-            cv[i] = __bfloat1622float2(c[i * 32 + lane]);
-            x = fmaf(qv[i].x, cv[i].x, fmaf(qv[i].y, cv[i].y, x));
-        }
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= scale;
-        const float mn = fmaxf(m, x);
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);
-        const float p = mn == -INFINITY ? 0.f : expf(x - mn);
-        l = l * f + p;
-        for (int i = 0; i < 8; ++i) {
-            acc[i].x = acc[i].x * f + p * cv[i].x;
-            acc[i].y = acc[i].y * f + p * cv[i].y;
-        }
-        m = mn;
-    }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint32_t*>(out + row * kDv)[i * 32 + lane] = pack_bf16x2(acc[i].x * inv, acc[i].y * inv);
-    if (lane == 0) lse[row] = l != 0.f ? m + logf(l) : -INFINITY;
-}
-
 // One warp per (sequence, key), over the sequence's rows and heads.
 __global__ void __launch_bounds__(256)
 mla_attn_mass_simple_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kv,

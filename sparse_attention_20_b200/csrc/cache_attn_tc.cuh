@@ -1,0 +1,916 @@
+// Dense MLA attention (MQA mode) of new tokens over the paged latent cache on
+// the 5th-generation tensor cores. Row t of sequence b = seq[t] at position
+// p = pos[t] sees V(t) = { s <= p }, with a window W > 0 only
+// { s <= p : s > p - W or s < sinks }, and
+//   x_s = scale q[t,h].c_s,  lse = log sum_V exp x_s,  out = sum_V exp(x_s - lse) c_s[0:512].
+//
+// A unit is up to 128 (row, head) pairs of consecutive rows of one sequence:
+// one row of 128 heads, eight rows of 16. Its keys are read in tiles of 128.
+// A cluster of two CTAs runs a unit as one pair MMA (cta_group::2, M = 128):
+// each CTA holds 64 of the pairs, so O (64 x 512 fp32, both lane halves of
+// 256 TMEM columns), S (64 columns) and two thirds of Q (192 columns) fit its
+// tensor memory, and the logits need no exchange. Per tile: S = Q C^T takes 36
+// MMAs of N = 128 (each CTA brings 64 of the keys, all 576 columns), O += P
+// C[:, 0:512] takes 16 of N = 256 (each CTA brings all 128 keys, its 256
+// columns). An N = 128 pair MMA takes 44.6 clocks here and an N = 256 one 64
+// (measured), whether A lies in TMEM or shared memory: 2630 clocks a tile,
+// 0.83 of the tensor pipe's peak. Keys cross L2 twice a tile (72 + 64 KB per
+// CTA); box loads of 24 to 32 KB reach 85 B/clk/SM from L2 and 7.4 TB/s from
+// HBM, single 8 KB ones 22 B/clk, so a tile is loaded in boxes of four slabs of
+// 64 columns x 64 keys, through one ring in the order the MMAs consume:
+//   K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1)
+// While the softmax of tile j runs, the tensor pipe does PV(j-1) and QK(j+1).
+//
+// Work is split evenly over the clusters: the units' tiles lie on one line
+// (with a constant per unit for its Q and its epilogue) that is cut into equal
+// pieces. A unit cut by a boundary leaves fp32 parts that a second kernel
+// joins in a fixed order; a cluster leaves at most two.
+//
+// Keys that some rows of a unit do not see: their logits are replaced by
+// -inf whatever the product gave, and where such a key's values hold a NaN or
+// an infinity, 0 times which would reach every row, those are zeroed in
+// shared memory before PV (a row that does see the key has a NaN logit).
+//
+// Warps (12 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
+// keys each), Q, epilogue; 8 loads; 9 MMA issue (even CTA); 10 passes the odd
+// CTA's "loaded" signals on to the even CTA; 11 idle.
+#pragma once
+#include <cuda.h>
+
+#include "cache_attn.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+namespace cache_attn {
+
+using namespace sm100;
+
+constexpr int kRows = 128;                 // (row, head) pairs of a unit
+constexpr int kTile = 128;                 // keys of a tile
+constexpr int kTcThreads = 384;
+constexpr int kSlab = 64 * 128;            // 64 rows x 64 columns bf16, 128B swizzle
+constexpr int kSlotBytes = 4 * kSlab;
+constexpr int kSlots = 5;
+constexpr int kQSlabsTmem = 6;             // columns [0, 384) of Q in TMEM, the rest in shared memory
+constexpr int kOffQ = 0;
+constexpr int kOffP = kOffQ + 3 * kSlab;
+constexpr int kOffRope = kOffP + 2 * kSlab;
+constexpr int kOffRing = kOffRope + 2 * kSlab;
+constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+constexpr int kOffRed = kOffBar + 512;                // [2][4][64] row maxima
+constexpr int kOffLsum = kOffRed + 2 * 4 * 64 * 4;    // [2][4][64] row sums
+constexpr int kOffPlan = kOffLsum + 2 * 4 * 64 * 4;
+constexpr int kTcSmem = kOffPlan + 256 + 1024;        // + alignment slack
+static_assert(kTcSmem <= 232448, "shared memory");
+
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
+
+enum : int {
+    B_FULL = 0, B_EMPTY = 5, B_PEER = 10, B_RFULL = 15, B_REMPTY = 17, B_RPEER = 19, B_QT = 21, B_SFULL = 22,
+    B_SFREE = 23, B_PFULL = 24, B_PVDONE = 25, B_RED = 26, B_LSUM = 28, B_DRAIN = 29, B_COUNT = 30
+};
+
+constexpr int kMaxClusters = 74;
+// A unit's Q, first softmax and epilogue cost about as much as this many tiles.
+constexpr int kUnitCost = 3;
+// Least work of a cluster: below it more clusters only add parts to join.
+constexpr int kMinWork = 8;
+
+// A split unit that the cluster of its last tile describes for the join.
+struct SplitDesc {
+    int t, n_rows;          // first row, (row, head) pairs (0: nothing to join)
+    int c_first, c_last;    // clusters that hold its parts
+    long long start, total; // its place on the line of work, the line's length
+    int ncl, pad;
+};
+
+// Workspace: [2 parts per cluster][128][512] fp32, their log2 sums, descriptors.
+constexpr size_t kPartBytes = (size_t)kMaxClusters * 2 * kRows * kDv * 4;
+constexpr size_t kPartLseBytes = (size_t)kMaxClusters * 2 * kRows * 4;
+constexpr size_t kWsBytes = kPartBytes + kPartLseBytes + kMaxClusters * sizeof(SplitDesc);
+
+struct Args {
+    PagedRows pg;
+    const int* pos;
+    int T, Hq, window, sinks;
+};
+
+// Rows t .. t + n - 1 of one sequence and the tiles of keys that they see.
+struct Unit {
+    int t, n, hi, min_hi, max_lo, sink_end;
+    int ns, m0, nt;                // sink tiles, first tile after them, tiles in all
+    const int* bt;
+    __device__ __forceinline__ int key0(int i) const { return (i < ns ? i : m0 + i - ns) * kTile; }
+    // every row sees keys [s, s + m)
+    __device__ __forceinline__ bool all_see(int s, int m) const
+    {
+        return s + m - 1 <= min_hi && (s >= max_lo || s + m <= sink_end);
+    }
+};
+
+__device__ __forceinline__ int rows_per_unit(int Hq) { return kRows / Hq; }
+
+__device__ __forceinline__ void finish_unit(Unit& u, int lo_min)
+{
+    u.ns = u.m0 = u.nt = 0;
+    if (u.hi < 0) return;
+    const int se = min(u.sink_end, u.hi + 1);
+    u.ns = (se + kTile - 1) / kTile;
+    u.m0 = max(u.ns, lo_min / kTile);
+    u.nt = u.ns + max(0, u.hi / kTile - u.m0 + 1);
+}
+
+// The unit that starts at row t (lanes = 32: a whole warp takes part; 1: one
+// thread). A run of more rows of a sequence is cut every rows_per_unit rows.
+template <int lanes>
+__device__ __forceinline__ Unit unit_at(const Args& a, int t)
+{
+    Unit u;
+    const int G = rows_per_unit(a.Hq), lane = lanes == 32 ? threadIdx.x & 31 : 0;
+    const int sq = a.pg.seq[t];
+    int lo_min = INT_MAX;
+    u.t = t;
+    u.n = 0;
+    u.hi = -1;
+    u.min_hi = INT_MAX;
+    u.max_lo = 0;
+    u.sink_end = a.window > 0 ? a.sinks : 0;
+    for (int g0 = 0; g0 < G; g0 += lanes) {
+        const int r = t + g0 + lane;
+        const bool in = g0 + lane < G && r < a.T && a.pg.seq[r] == sq;
+        int cnt = in ? 1 : 0;
+        if (lanes == 32) {
+            const unsigned m = __ballot_sync(0xffffffffu, in);
+            cnt = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        }
+        if (lane < cnt) {
+            long long base;
+            const int* bt;
+            const int n = row_keys(a.pg, a.pos, nullptr, r, a.T, 0, &base, &bt);
+            u.min_hi = min(u.min_hi, n - 1);
+            if (n > 0) {
+                const Visible v = visible_of(n, a.pos[r], a.window, a.sinks);
+                u.hi = max(u.hi, v.hi);
+                u.max_lo = max(u.max_lo, v.lo);
+                lo_min = min(lo_min, v.lo);
+            }
+        }
+        u.n += cnt;
+        if (cnt < lanes) break;
+    }
+    if (lanes == 32) {
+        u.hi = __reduce_max_sync(0xffffffffu, u.hi);
+        u.min_hi = __reduce_min_sync(0xffffffffu, u.min_hi);
+        u.max_lo = __reduce_max_sync(0xffffffffu, u.max_lo);
+        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    }
+    u.bt = a.pg.block_table + (size_t)(u.hi >= 0 ? sq : 0) * a.pg.max_pages;
+    finish_unit(u, lo_min);
+    return u;
+}
+
+// This cluster's piece [w0, w1) of the line of work, and the unit it starts in.
+struct Piece {
+    long long w0, w1, total, first_start;
+    int first_t, ncl;
+    __device__ __forceinline__ int cluster_of(long long x) const { return (int)(((x + 1) * ncl - 1) / total); }
+    __device__ __forceinline__ static long long begin(long long total, int ncl, int c) { return total * c / ncl; }
+};
+
+// Block-wide: finds the units' places on the line of work from seq and pos
+// (every CTA does so for itself; a row costs a thread a few loads).
+__device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
+{
+    long long* s64 = reinterpret_cast<long long*>(smem);       // [12] warp sums, then the piece
+    int* s32 = reinterpret_cast<int*>(smem + 128);             // [12] last run start of each warp's rows
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kTcThreads / 32;
+    const int G = rows_per_unit(a.Hq);
+    const int per = ceil_div(a.T, kTcThreads);
+    const int r0 = min(a.T, tid * per), r1 = min(a.T, r0 + per);
+    auto breaks = [&](int t) { return t == 0 || a.pg.seq[t] != a.pg.seq[t - 1]; };
+    // start of the run that row r0 lies in: the last break before or at it
+    int last = -1;
+    for (int t = r0; t < r1; ++t)
+        if (breaks(t)) last = t;
+    int run = last;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run = max(run, y);
+    }
+    if (lane == 31) s32[warp] = run;
+    __syncthreads();
+    int before = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) before = -1;
+    for (int w = 0; w < warp; ++w) before = max(before, s32[w]);
+    // work of the units that start in this thread's rows
+    auto walk = [&](auto&& f) {
+        int start = before;
+        for (int t = r0; t < r1; ++t) {
+            if (breaks(t)) start = t;
+            if ((t - start) % G == 0) f(t, unit_at<1>(a, t).nt + kUnitCost);
+        }
+    };
+    long long sum = 0;
+    walk([&](int, int w) { sum += w; });
+    long long pre = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
+    }
+    if (lane == 31) s64[warp] = pre;
+    __syncthreads();
+    Piece p;
+    p.total = 0;
+    long long base = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += s64[w];
+        p.total += s64[w];
+    }
+    pre += base - sum;
+    p.ncl = (int)max(1ll, min((long long)clusters, p.total / kMinWork));
+    p.w0 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid) : p.total;
+    p.w1 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid + 1) : p.total;
+    __syncthreads();
+    if (p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum) {
+        long long at = pre;
+        bool found = false;
+        walk([&](int t, int w) {
+            if (!found && p.w0 < at + w) {
+                found = true;
+                s64[0] = at;
+                s32[0] = t;
+            }
+            at += w;
+        });
+    }
+    __syncthreads();
+    p.first_start = s64[0];
+    p.first_t = s32[0];
+    return p;
+}
+
+// A cluster's share of a unit: its tiles [a, b).
+struct Part {
+    Unit u;
+    long long start;
+    int a, b;
+    bool owns_empty;       // a unit without keys, to be written as zeros
+    __device__ __forceinline__ bool split() const { return a > 0 || b < u.nt; }
+};
+
+// Walks the parts of a piece (a whole warp takes part).
+struct Walk {
+    long long at;
+    int t;
+    __device__ __forceinline__ Walk(const Piece& p) : at(p.first_start), t(p.first_t) {}
+    __device__ __forceinline__ bool next(const Args& a, const Piece& pc, Part& p)
+    {
+        while (at < pc.w1 && t < a.T && pc.w0 < pc.w1) {
+            p.u = unit_at<32>(a, t);
+            p.start = at;
+            const long long d = at + kUnitCost;
+            p.a = (int)max(0ll, min((long long)p.u.nt, pc.w0 - d));
+            p.b = (int)max(0ll, min((long long)p.u.nt, pc.w1 - d));
+            p.owns_empty = p.u.nt == 0 && at >= pc.w0;
+            at = d + p.u.nt;
+            t += p.u.n;
+            if (p.a < p.b || p.owns_empty) return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
+{
+    return __all_sync(0xffffffffu, mbar_wait<true>(bar, par, abort_flag, tag, c));
+}
+
+// Bits of the 32 keys from s that the row sees.
+__device__ __forceinline__ uint32_t seen_bits(const Visible& v, int s)
+{
+    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+    return below(v.hi + 1 - s) & (~below(v.lo - s) | below(v.sink_end - s));
+}
+
+// Non-finite bf16 halves of w -> 0.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w)
+{
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __grid_constant__ CUtensorMap tm_kv1,
+                         const __nv_bfloat16* __restrict__ q, const Args args, float scale_log2,
+                         __nv_bfloat16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
+                         float* __restrict__ part_lse, SplitDesc* __restrict__ desc)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* sgen = smem_raw + (sbase - raw);
+    const uint32_t bar0 = sbase + kOffBar;
+    uint32_t* taddr_slot = reinterpret_cast<uint32_t*>(sgen + kOffBar + 8 * B_COUNT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + kOffBar + 8 * B_COUNT + 8);
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cid = (int)(blockIdx.x >> 1), clusters = (int)(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(bar(B_FULL + s), 1);
+            mbar_init(bar(B_EMPTY + s), 1);
+            mbar_init(bar(B_PEER + s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(B_RFULL + b), 1);
+            mbar_init(bar(B_REMPTY + b), 1);
+            mbar_init(bar(B_RPEER + b), 1);
+            mbar_init(bar(B_RED + b), 8);
+        }
+        // the softmax warps of both CTAs
+        mbar_init(bar(B_QT), 16);
+        mbar_init(bar(B_SFREE), 16);
+        mbar_init(bar(B_PFULL), 16);
+        mbar_init(bar(B_SFULL), 1);
+        mbar_init(bar(B_PVDONE), 1);
+        mbar_init(bar(B_LSUM), 8);
+        mbar_init(bar(B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init_cluster();
+    }
+    if (warp == 9) {
+        tmem_alloc_pair(smem_u32(taddr_slot), 512);
+        tmem_relinquish_pair();
+    }
+    griddep_wait();
+    const Piece pc = plan(args, cid, clusters, sgen + kOffPlan);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers exist before any remote arrival
+    tc_fence_after();
+    const uint32_t tmem = *taddr_slot;
+    bool issued_any = false;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            prefetch_tmap(&tm_kv4);
+            prefetch_tmap(&tm_kv1);
+        }
+        if (rank == 0 && lane == 0) desc[cid].n_rows = 0;
+        int slot = 0, rslot = 0, issued = 0, rissued = 0;
+        uint32_t ph = 0, rph = 0;
+        bool ok = true;
+        // one box of four slabs (columns 64 * z ..) of 64 cache rows from `row`
+        auto push = [&](int row, int z) {
+            if (!ok) return;
+            ok = mbar_wait<true>(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, issued);
+            if (!ok) return;
+            mbar_arrive_expect_tx(bar(B_FULL + slot), kSlotBytes);
+            tma_load_3d(sbase + kOffRing + slot * kSlotBytes, &tm_kv4, 0, row, z, bar(B_FULL + slot));
+            ++issued;
+            if (++slot == kSlots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        };
+        Walk walk(pc);
+        Part p;
+        while (ok && walk.next(args, pc, p)) {
+            if (p.a >= p.b) continue;
+            if (rank == 0 && lane == 0 && p.b == p.u.nt && p.a > 0) {
+                SplitDesc d;
+                d.t = p.u.t;
+                d.n_rows = p.u.n * args.Hq;
+                d.c_first = pc.cluster_of(p.start + kUnitCost);
+                d.c_last = cid;
+                d.start = p.start;
+                d.total = pc.total;
+                d.ncl = pc.ncl;
+                d.pad = 0;
+                desc[cid] = d;
+            }
+            // cache rows of the tiles' two blocks of 64 keys, sixteen tiles at a
+            // time over the lanes (a block behind the last key reads the one before)
+            int rows_l = 0, pa = 0, pb = 0;
+            for (int j = p.a; j < p.b; ++j) {
+                if (((j - p.a) & 15) == 0) {
+                    const int jj = min(j + (lane >> 1), p.b - 1);
+                    int s = p.u.key0(jj) + (lane & 1) * 64;
+                    if (s > p.u.hi) s -= 64;
+                    rows_l = (int)key_row(args.pg, p.u.bt, 0, s);
+                }
+                const int e = ((j - p.a) & 15) * 2;
+                const int ra = __shfl_sync(0xffffffffu, rows_l, e), rb = __shfl_sync(0xffffffffu, rows_l, e + 1);
+                if (lane == 0) {
+                    const int own = rank ? rb : ra;
+                    push(own, 0);
+                    push(own, 4);
+                    if (ok) ok = mbar_wait<true>(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, rissued);
+                    if (ok) {
+                        mbar_arrive_expect_tx(bar(B_RFULL + rslot), kSlab);
+                        tma_load_3d(sbase + kOffRope + rslot * kSlab, &tm_kv1, 0, own, 8, bar(B_RFULL + rslot));
+                        ++rissued;
+                        rslot ^= 1;
+                        if (rslot == 0) rph ^= 1u;
+                    }
+                    if (j > p.a) {
+                        push(pa, 4 * (int)rank);
+                        push(pb, 4 * (int)rank);
+                    }
+                    if (j == p.b - 1) {
+                        push(ra, 4 * (int)rank);
+                        push(rb, 4 * (int)rank);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                pa = ra;
+                pb = rb;
+            }
+        }
+        if (!ok && lane == 0) {
+            // copies in flight land before the CTA gives its shared memory up
+            const uint64_t t0 = globaltimer_ns();
+            for (int i = max(0, issued - kSlots); i < issued; ++i)
+                while (!mbar_try_wait(bar(B_FULL + i % kSlots), (i / kSlots) & 1) &&
+                       globaltimer_ns() - t0 < kWaitLimitNs) {
+                }
+            for (int i = max(0, rissued - 2); i < rissued; ++i)
+                while (!mbar_try_wait(bar(B_RFULL + (i & 1)), (i >> 1) & 1) &&
+                       globaltimer_ns() - t0 < kWaitLimitNs) {
+                }
+        }
+    } else if (warp == 10 && rank == 1) {
+        // ------------------------------- "loaded" signals of the odd CTA, passed on
+        int slot = 0, rslot = 0, n = 0;
+        uint32_t ph = 0, rph = 0;
+        bool ok = true;
+        auto pass = [&]() {
+            if (!ok) return;
+            ok = mbar_wait<true>(bar(B_FULL + slot), ph, abort_flag, 1100 + slot, n);
+            if (!ok) return;
+            mbar_arrive_cluster(mapa(bar(B_PEER + slot), 0));
+            if (++slot == kSlots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        };
+        Walk walk(pc);
+        Part p;
+        while (ok && walk.next(args, pc, p)) {
+            for (int j = p.a; j < p.b && ok; ++j, ++n) {
+                if (lane == 0) {
+                    pass();
+                    pass();
+                    if (ok) ok = mbar_wait<true>(bar(B_RFULL + rslot), rph, abort_flag, 1110 + rslot, n);
+                    if (ok) {
+                        mbar_arrive_cluster(mapa(bar(B_RPEER + rslot), 0));
+                        rslot ^= 1;
+                        if (rslot == 0) rph ^= 1u;
+                    }
+                    if (j > p.a) {
+                        pass();
+                        pass();
+                    }
+                    if (j == p.b - 1) {
+                        pass();
+                        pass();
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            }
+        }
+    } else if (warp == 9 && rank == 0) {
+        // ---------------------------------------------------------- MMA issue
+        const uint32_t id_qk = idesc_bf16(128, kTile, false), id_pv = idesc_bf16(128, 256, true);
+        const uint64_t d_k = smem_desc(sbase + kOffRing, 16, 1024, kSwizzle128B);
+        const uint64_t d_v = smem_desc(sbase + kOffRing, kSlab, 1024, kSwizzle128B);
+        const uint64_t d_r = smem_desc(sbase + kOffRope, 16, 1024, kSwizzle128B);
+        const uint64_t d_q = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+        const uint64_t d_p = smem_desc(sbase + kOffP, 16, 1024, kSwizzle128B);
+        int slot = 0, rslot = 0, g = 0, n_units = 0;
+        uint32_t ph = 0, rph = 0;
+        bool ok = true;
+        auto loaded = [&]() -> bool {
+            return mbar_wait<true>(bar(B_FULL + slot), ph, abort_flag, 1200 + slot, g) &&
+                   mbar_wait<true>(bar(B_PEER + slot), ph, abort_flag, 1210 + slot, g);
+        };
+        auto done = [&]() {
+            mma_commit_pair(bar(B_EMPTY + slot));
+            if (++slot == kSlots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        };
+        // S = Q C^T of tile g
+        auto qk = [&]() -> bool {
+            if (g > 0 && !mbar_wait<true>(bar(B_SFREE), (g - 1) & 1, abort_flag, 1220, g)) return false;
+            if (!loaded()) return false;
+            tc_fence_after();
+            uint64_t b = d_k + (uint64_t)(slot * (kSlotBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk)
+                mma_pair_ts(tmem + kColS, tmem + kColQ + kk * 8, b + (kk >> 2) * (kSlab >> 4) + (kk & 3) * 2, id_qk,
+                            kk > 0 ? 1u : 0u);
+            done();
+            if (!loaded()) return false;
+            tc_fence_after();
+            b = d_k + (uint64_t)(slot * (kSlotBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk) {
+                const uint64_t bk = b + (kk >> 2) * (kSlab >> 4) + (kk & 3) * 2;
+                if (kk < 8)
+                    mma_pair_ts(tmem + kColS, tmem + kColQ + (16 + kk) * 8, bk, id_qk, 1u);
+                else
+                    mma_pair_ss(tmem + kColS, d_q + ((kk - 8) >> 2) * (kSlab >> 4) + (kk & 3) * 2, bk, id_qk, 1u);
+            }
+            done();
+            if (!mbar_wait<true>(bar(B_RFULL + rslot), rph, abort_flag, 1230, g) ||
+                !mbar_wait<true>(bar(B_RPEER + rslot), rph, abort_flag, 1231, g))
+                return false;
+            tc_fence_after();
+            b = d_r + (uint64_t)(rslot * (kSlab >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_pair_ss(tmem + kColS, d_q + 2 * (kSlab >> 4) + kk * 2, b + kk * 2, id_qk, 1u);
+            mma_commit_pair(bar(B_REMPTY + rslot));
+            rslot ^= 1;
+            if (rslot == 0) rph ^= 1u;
+            mma_commit_pair(bar(B_SFULL));
+            return true;
+        };
+        // O (+)= P C[:, 0:512] of tile gp
+        auto pv = [&](int gp, bool first) -> bool {
+            if (!mbar_wait<true>(bar(B_PFULL), gp & 1, abort_flag, 1240, gp)) return false;
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                if (!loaded()) return false;
+                tc_fence_after();
+                const uint64_t b = d_v + (uint64_t)(slot * (kSlotBytes >> 4));
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_pair_ss(tmem + kColO + n * 128, d_p + blk * (kSlab >> 4) + kk * 2,
+                                    b + n * (2 * kSlab >> 4) + kk * (16 * 128 >> 4), id_pv,
+                                    first && blk == 0 && kk == 0 ? 0u : 1u);
+                done();
+            }
+            mma_commit_pair(bar(B_PVDONE));
+            return true;
+        };
+        Walk walk(pc);
+        Part p;
+        while (ok && walk.next(args, pc, p)) {
+            if (p.a >= p.b) continue;
+            if (lane == 0) {
+                ok = mbar_wait<true>(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
+                const int nt = p.b - p.a;
+                for (int j = 0; j < nt && ok; ++j) {
+                    ok = qk();
+                    issued_any = true;
+                    ++g;
+                    if (ok && j > 0) ok = pv(g - 2, j == 1);
+                }
+                if (ok) ok = pv(g - 1, nt == 1);
+            }
+            ++n_units;
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+    } else if (warp < 8) {
+        // ----------------------------------------- softmax, Q, epilogue
+        // TMEM lane i holds pair i % 64 of this CTA's 64: keys of the tile's first
+        // block of 64 (and output columns 0..255) for i < 64, of the second (and
+        // columns 256..511) for the others; hs halves both once more.
+        const int hs = warp >> 2;
+        const int i = (warp & 3) * 32 + lane;
+        const int side = i >> 6, lr = i & 63;
+        const int r = (int)rank * 64 + lr;                  // pair of the unit
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const int grp = side * 2 + hs;
+        float* red = reinterpret_cast<float*>(sgen + kOffRed);
+        float* lsum_s = reinterpret_cast<float*>(sgen + kOffLsum);
+        const uint32_t qt0 = mapa(bar(B_QT), 0), sfree0 = mapa(bar(B_SFREE), 0), pfull0 = mapa(bar(B_PFULL), 0);
+        const size_t all_rows = (size_t)args.T * args.Hq;
+        bool ok = true;
+        // Q of a unit: columns [0, 384) to TMEM (row i % 64 in both lanes), the
+        // others to shared memory
+        auto write_q = [&](int t) {
+            const size_t row0 = (size_t)t * args.Hq;
+            const uint4* src = reinterpret_cast<const uint4*>(q + min(row0 + r, all_rows - 1) * kDqk + 192 * hs);
+            uint4 tail[6];
+#pragma unroll
+            for (int it = 0; it < 6; ++it) {
+                const int p = it * 256 + (int)threadIdx.x;
+                tail[it] = __ldg(reinterpret_cast<const uint4*>(
+                                     q + min(row0 + rank * 64 + p / 24, all_rows - 1) * kDqk + 384) + p % 24);
+            }
+#pragma unroll
+            for (int b = 0; b < 3; ++b) {
+                uint32_t w[32];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    const uint4 x = __ldg(src + 8 * b + v);
+                    w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
+                }
+                tmem_st32(tmem + lane_addr + kColQ + 96 * hs + 32 * b, w);
+            }
+#pragma unroll
+            for (int it = 0; it < 6; ++it) {
+                const int p = it * 256 + (int)threadIdx.x, row = p / 24, c = p % 24;
+                st_shared_v4(sbase + kOffQ + (c >> 3) * kSlab + row * 128 + (((c & 7) ^ (row & 7)) << 4), tail[it]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(qt0);
+        };
+        auto out_row = [&](const Unit& u) {
+            return out + ((size_t)u.t * args.Hq + r) * kDv + side * 256 + 128 * hs;
+        };
+        // the next part with keys; units without any are written on the way
+        Walk walk(pc);
+        auto advance = [&](Part& p) -> bool {
+            while (walk.next(args, pc, p)) {
+                if (p.a < p.b) return true;
+                if (r < p.u.n * args.Hq) {
+                    uint4* dst = reinterpret_cast<uint4*>(out_row(p.u));
+                    for (int v = 0; v < 16; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (grp == 0) lse[(size_t)p.u.t * args.Hq + r] = -INFINITY;
+                }
+                __syncwarp();
+            }
+            return false;
+        };
+        Part cur, nxt;
+        bool have = advance(cur);
+        if (have) write_q(cur.u.t);
+        int g = 0, ring = 0, uc = 0;
+        while (have && ok) {
+            const Unit& u = cur.u;
+            const int nt = cur.b - cur.a;
+            const bool live = r < u.n * args.Hq;
+            Visible vis;
+            vis.hi = -1;
+            vis.lo = vis.sink_end = 0;
+            if (live) {
+                long long base;
+                const int* bt;
+                const int t = u.t + r / args.Hq;
+                const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
+                if (n > 0) vis = visible_of(n, args.pos[t], args.window, args.sinks);
+            }
+            const bool more = advance(nxt);
+            if (more) {
+                const char* qn = reinterpret_cast<const char*>(q + min((size_t)nxt.u.t * args.Hq + r, all_rows - 1) * kDqk);
+                for (int o = grp * 128; o < kDqk * 2; o += 512)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(qn + o));
+            }
+            float m_use = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j, ++g) {
+                const int key0 = u.key0(cur.a + j);
+                const bool whole = u.all_see(key0, kTile);
+                if (!wait_all(bar(B_SFULL), g & 1, abort_flag, 1300, g)) { ok = false; break; }
+                tc_fence_after();
+                float x[32];
+                {
+                    uint32_t sr[32];
+                    tmem_ld32(tmem + lane_addr + kColS + 32 * hs, sr);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(sfree0);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(sr[e]) * scale_log2;
+                }
+                if (!whole) {
+                    const uint32_t bits = seen_bits(vis, key0 + 64 * side + 32 * hs);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) x[e] = -INFINITY;
+                }
+                float mx[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) mx[e] = fmaxf(x[e], x[e + 16]);
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
+                // row maximum over the four threads that share the row
+                float* rd = red + (g & 1) * 256;
+                rd[grp * 64 + lr] = mx[0];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_RED + (g & 1)));
+                if (!wait_all(bar(B_RED + (g & 1)), (g >> 1) & 1, abort_flag, 1310, g)) { ok = false; break; }
+                const float m_new = fmaxf(m_use, fmaxf(fmaxf(rd[lr], rd[64 + lr]), fmaxf(rd[128 + lr], rd[192 + lr])));
+                // the running maximum follows only when it would let P exceed 2^8
+                const bool raise = m_new > m_use + 8.f;
+                const bool rescale = raise && m_use != -INFINITY;
+                const float f = rescale ? ex2(m_use - m_new) : 1.f;
+                if (raise) m_use = m_new;
+                const float msub = m_use == -INFINITY ? 0.f : m_use;
+                // P goes to the MMA in bf16 (half a step is 2^-9 of each weight, below
+                // the output's own rounding); its sum is taken before, in fp32
+                uint32_t pk[16];
+                float ps[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p0 = ex2(x[2 * e] - msub), p1 = ex2(x[2 * e + 1] - msub);
+                    ps[e] = p0 + p1;
+                    pk[e] = pack_bf16x2(p0, p1);
+                }
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int e = 0; e < w; ++e) ps[e] += ps[e + w];
+                l = l * f + ps[0];
+                // PV(g-1) has read P and written O
+                if (j > 0 && !wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1320, g)) { ok = false; break; }
+                if (__any_sync(0xffffffffu, rescale)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        uint32_t o[32];
+                        const uint32_t ta = tmem + lane_addr + kColO + 128 * hs + q4 * 32;
+                        tmem_ld32(ta, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(ta, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    st_shared_v4(sbase + kOffP + side * kSlab + lr * 128 + (((4 * hs + m) ^ (lr & 7)) << 4),
+                                 make_uint4(pk[4 * m], pk[4 * m + 1], pk[4 * m + 2], pk[4 * m + 3]));
+                if (!whole) {
+                    // ring places of this tile's values: behind the next tile's keys
+                    const int v0 = ring + 4 * j + (j < nt - 1 ? 4 : 2);
+#pragma unroll 1
+                    for (int blk = 0; blk < 2; ++blk) {
+                        const int rs = (v0 + blk) % kSlots;
+                        if (!wait_all(bar(B_FULL + rs), ((v0 + blk) / kSlots) & 1, abort_flag, 1330, g)) { ok = false; break; }
+                        uint8_t* slab = sgen + kOffRing + rs * kSlotBytes;
+                        const int row = (threadIdx.x >> 3) & 31;
+#pragma unroll 1
+                        for (int rr = row; rr < 64; rr += 32) {
+                            if (u.all_see(key0 + 64 * blk + rr, 1)) continue;
+#pragma unroll
+                            for (int sl = 0; sl < 4; ++sl) {
+                                uint4* v = reinterpret_cast<uint4*>(slab + sl * kSlab + rr * 128) + (threadIdx.x & 7);
+                                const uint4 w = *v;
+                                const uint4 c = make_uint4(finite_halves(w.x), finite_halves(w.y), finite_halves(w.z),
+                                                           finite_halves(w.w));
+                                if (c.x != w.x || c.y != w.y || c.z != w.z || c.w != w.w) *v = c;
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(pfull0);
+            }
+            ring += 4 * nt;
+            if (!ok) break;
+            // every QK of this unit has completed: Q makes room for the next unit's
+            if (more) write_q(nxt.u.t);
+            // row sum over the four threads of the row
+            lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_LSUM));
+            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g)) { ok = false; break; }
+            const float* ls = lsum_s + (uc & 1) * 256 + lr;
+            l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
+            if (!wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1350, g)) { ok = false; break; }
+            tc_fence_after();
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const float lv = l != 0.f ? m_use + __log2f(l) : -INFINITY;
+            const bool split = cur.split();
+            const size_t prow = ((size_t)cid * 2 + (cur.start < pc.w0 ? 0 : 1)) * kRows + r;
+            float* po = part_o + prow * kDv + side * 256 + 128 * hs;
+            __nv_bfloat16* orow = out_row(u);
+#pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_addr + kColO + 128 * hs + q4 * 32, o);
+                tmem_wait_ld();
+                if (live && split) {
+                    float4* dst = reinterpret_cast<float4*>(po + q4 * 32);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                             __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+                } else if (live) {
+                    uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                               __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+                        dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            // O is read: the next unit's first PV overwrites it once this warp
+            // hands over its first P
+            tc_fence_before();
+            if (live && grp == 0) {
+                if (split)
+                    part_lse[prow] = lv;
+                else
+                    lse[(size_t)u.t * args.Hq + r] = lv * 0.69314718055994531f;
+            }
+            cur = nxt;
+            have = more;
+            ++uc;
+        }
+    }
+
+    if (warp == 9 && lane == 0 && issued_any) {
+        // every MMA issued completes before TMEM is released
+        mma_commit_pair(bar(B_DRAIN));
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar(B_DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' MMAs, remote arrivals and copies are over
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc_pair(tmem, 512);
+    cluster_sync();
+}
+
+// Joins the parts of a split unit, in the order of the clusters:
+//   lse = log sum_z 2^lse_z,  out = sum_z 2^(lse_z - lse) o_z.
+// One CTA per (cluster that ended a split unit, 8 of its pairs).
+constexpr int kJoinRows = 8;
+
+__global__ void __launch_bounds__(128)
+mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                           const SplitDesc* __restrict__ desc, int Hq, __nv_bfloat16* __restrict__ out,
+                           float* __restrict__ lse)
+{
+    __shared__ float wz[kJoinRows][kMaxClusters];
+    __shared__ int where[kMaxClusters];
+    griddep_wait();
+    const SplitDesc d = desc[blockIdx.x];
+    const int r0 = blockIdx.y * kJoinRows;
+    if (d.n_rows <= r0) return;
+    const int parts = d.c_last - d.c_first + 1;
+    for (int z = threadIdx.x; z < parts; z += 128) {
+        const int c = d.c_first + z;
+        where[z] = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < kJoinRows && r0 + threadIdx.x < d.n_rows) {
+        const int r = r0 + threadIdx.x;
+        float m = -INFINITY;
+        for (int z = 0; z < parts; ++z) {
+            const float v = part_lse[where[z] * kRows + r];
+            wz[threadIdx.x][z] = v;
+            m = fmaxf(m, v);
+        }
+        float l = 0.f;
+        const float ms = m == -INFINITY ? 0.f : m;
+        for (int z = 0; z < parts; ++z) l += exp2f(wz[threadIdx.x][z] - ms);
+        const float total = l != 0.f ? ms + log2f(l) : -INFINITY;
+        for (int z = 0; z < parts; ++z) {
+            const float v = wz[threadIdx.x][z];
+            wz[threadIdx.x][z] = v == -INFINITY ? 0.f : exp2f(v - total);
+        }
+        lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kJoinRows * kDv / 4; e += 128) {
+        const int rr = e / (kDv / 4), c4 = e % (kDv / 4);
+        if (r0 + rr >= d.n_rows) break;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int z = 0; z < parts; ++z) {
+            const float w = wz[rr][z];
+            const float4 v = reinterpret_cast<const float4*>(part_o + ((size_t)where[z] * kRows + r0 + rr) * kDv)[c4];
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4] =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    }
+}
+
+}  // namespace cache_attn
+}  // namespace dsa

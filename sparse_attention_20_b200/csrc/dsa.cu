@@ -20,6 +20,7 @@
 #include "attn_simple.cuh"
 #include "attn_tc.cuh"
 #include "cache_attn.cuh"
+#include "cache_attn_tc.cuh"
 #include "cache_evict.cuh"
 #include "common.cuh"
 #include "debug_checks.cuh"
@@ -738,6 +739,23 @@ int make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t row
     return DSA_OK;
 }
 
+// A row-major bf16 [rows, 64 * slabs] matrix as [slabs][rows][64]: a box holds
+// box_slabs slabs of 64 columns x 64 rows, each in 128B-swizzled order.
+int make_tmap_slabs(CUtensorMap* m, const void* base, uint64_t slabs, uint64_t rows, uint32_t box_slabs)
+{
+    const cuuint64_t dims[3] = {64, rows, slabs};
+    const cuuint64_t strides[2] = {slabs * 128, 128};
+    const cuuint32_t box[3] = {64, 64, box_slabs};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return DSA_OK;
+}
+
 int attn_tc(const __nv_bfloat16* q, const __nv_bfloat16* kv, const int32_t* idx,
             const int32_t* pos, const int32_t* k_base, int T, int S, int k, float scale,
             __nv_bfloat16* out, float* lse, cudaStream_t st, const dsa::PagedRows& pg = {},
@@ -1163,6 +1181,8 @@ int check_cache_attn(const void* q, const void* kv_pages, int num_pages, int pag
     if ((long long)T * Hq > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T * Hq = %lld", (long long)T * Hq);
     if (d_qk != dsa::cache_attn::kDqk)
         return fail(DSA_ERR_UNSUPPORTED, "d_qk=%d (supported: %d)", d_qk, dsa::cache_attn::kDqk);
+    if ((long long)max_pages * page_size > (1 << 30))
+        return fail(DSA_ERR_UNSUPPORTED, "a table of %lld keys (supported: up to 2^30)", (long long)max_pages * page_size);
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
         return fail(DSA_ERR_ARG, "window=%d, sinks=%d (both >= 0; sinks only with a window)", window, sinks);
     return DSA_OK;
@@ -1185,7 +1205,7 @@ dsa::PagedRows paged_rows(const int32_t* block_table, const int32_t* seq, int n_
 size_t dsa_mla_attn_paged_workspace_size(int T, int Hq)
 {
     if (T <= 0 || Hq <= 0) return 0;
-    return 0;
+    return dsa::cache_attn::kWsBytes;
 }
 
 int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
@@ -1204,11 +1224,38 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     if (need && (!workspace || ws_bytes < need || !al16(workspace)))
         return fail(DSA_ERR_WORKSPACE, "paged attention needs %zu workspace bytes (got %zu)", need, ws_bytes);
     const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
-    const long long rows = (long long)T * Hq;
-    mla_attn_paged_simple_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(kv_pages), pg, pos, T, Hq,
-        scale, window, sinks, reinterpret_cast<__nv_bfloat16*>(out), lse);
-    DSA_LAUNCH_CHECK("mla_attn_paged_simple_kernel");
+    CUtensorMap tm4, tm1;
+    const uint64_t pool_rows = (uint64_t)num_pages * page_size;
+    if (int rc = make_tmap_slabs(&tm4, kv_pages, kDqk / 64, pool_rows, 4)) return rc;
+    if (int rc = make_tmap_slabs(&tm1, kv_pages, kDqk / 64, pool_rows, 1)) return rc;
+    cudaError_t e = cudaFuncSetAttribute(mla_attn_paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kTcSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_attn_paged_tc_kernel)");
+    Args args;
+    args.pg = pg;
+    args.pos = pos;
+    args.T = T;
+    args.Hq = Hq;
+    args.window = window;
+    args.sinks = sinks;
+    float* part_o = reinterpret_cast<float*>(workspace);
+    float* part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kPartBytes);
+    SplitDesc* desc = reinterpret_cast<SplitDesc*>(reinterpret_cast<char*>(workspace) + kPartBytes + kPartLseBytes);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // the most work there can be bounds the clusters with a piece of it
+    const long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
+    const long long work = T * (tiles + kUnitCost);
+    const int clusters = (int)std::max(1ll, std::min<long long>(work / kMinWork,
+                                                                std::min(kMaxClusters, std::max(1, num_sms() / 2))));
+    launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1,
+               reinterpret_cast<const __nv_bfloat16*>(q), args, scale * 1.4426950408889634f,
+               reinterpret_cast<__nv_bfloat16*>(out), lse, part_o, part_lse, desc);
+    DSA_LAUNCH_CHECK("mla_attn_paged_tc_kernel");
+    if (clusters > 1) {
+        launch_pdl(mla_attn_paged_join_kernel, dim3(clusters, kRows / kJoinRows), dim3(128), 0, st, part_o, part_lse,
+                   desc, Hq, reinterpret_cast<__nv_bfloat16*>(out), lse);
+        DSA_LAUNCH_CHECK("mla_attn_paged_join_kernel");
+    }
     return DSA_OK;
 }
 
