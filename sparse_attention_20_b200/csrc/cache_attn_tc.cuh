@@ -31,9 +31,8 @@
 // an infinity, 0 times which would reach every row, those are zeroed in
 // shared memory before PV (a row that does see the key has a NaN logit).
 //
-// Warps (12 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
-// keys each), Q, epilogue; 8 loads; 9 MMA issue (even CTA); 10 passes the odd
-// CTA's "loaded" signals on to the even CTA; 11 idle.
+// Warps (10 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
+// keys each), Q, epilogue; 8 loads; 9 MMA issue (even CTA).
 #pragma once
 #include <cuda.h>
 
@@ -47,7 +46,7 @@ using namespace sm100;
 
 constexpr int kRows = 128;                 // (row, head) pairs of a unit
 constexpr int kTile = 128;                 // keys of a tile
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 320;
 constexpr int kSlab = 64 * 128;            // 64 rows x 64 columns bf16, 128B swizzle
 constexpr int kSlotBytes = 4 * kSlab;
 constexpr int kSlots = 5;
@@ -65,9 +64,12 @@ static_assert(kTcSmem <= 232448, "shared memory");
 
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
+// On the even CTA's barriers: FULL, RFULL (bytes of both CTAs), QT, SFREE, PFULL
+// (arrivals of both). VCUT: a slot with values of a tile that not every row
+// sees whole, on each CTA's own.
 enum : int {
-    B_FULL = 0, B_EMPTY = 5, B_PEER = 10, B_RFULL = 15, B_REMPTY = 17, B_RPEER = 19, B_QT = 21, B_SFULL = 22,
-    B_SFREE = 23, B_PFULL = 24, B_PVDONE = 25, B_RED = 26, B_LSUM = 28, B_DRAIN = 29, B_COUNT = 30
+    B_FULL = 0, B_EMPTY = 5, B_VCUT = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
+    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_COUNT = 28
 };
 
 constexpr int kMaxClusters = 74;
@@ -181,8 +183,8 @@ struct Piece {
 // (every CTA does so for itself; a row costs a thread a few loads).
 __device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
 {
-    long long* s64 = reinterpret_cast<long long*>(smem);       // [12] warp sums, then the piece
-    int* s32 = reinterpret_cast<int*>(smem + 128);             // [12] last run start of each warp's rows
+    long long* s64 = reinterpret_cast<long long*>(smem);       // [10] warp sums, then the piece
+    int* s32 = reinterpret_cast<int*>(smem + 128);             // [10] last run start of each warp's rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kTcThreads / 32;
     const int G = rows_per_unit(a.Hq);
@@ -286,6 +288,24 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile in
     return __all_sync(0xffffffffu, mbar_wait<true>(bar, par, abort_flag, tag, c));
 }
 
+// Waits on a barrier per lane, all at once (one round costs about as much as a
+// wait on one barrier). Bounded; the outcome is the warp's.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
+{
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, par))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        bool mine = mbar_test_wait(bar, par);
+        if (__all_sync(0xffffffffu, mine)) return true;
+        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late && !mine) report_timeout(tag, c, (int)par);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
 // Bits of the 32 keys from s that the row sees.
 __device__ __forceinline__ uint32_t seen_bits(const Visible& v, int s)
 {
@@ -323,12 +343,11 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(bar(B_FULL + s), 1);
             mbar_init(bar(B_EMPTY + s), 1);
-            mbar_init(bar(B_PEER + s), 1);
+            mbar_init(bar(B_VCUT + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(B_RFULL + b), 1);
             mbar_init(bar(B_REMPTY + b), 1);
-            mbar_init(bar(B_RPEER + b), 1);
             mbar_init(bar(B_RED + b), 8);
         }
         // the softmax warps of both CTAs
@@ -355,24 +374,37 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
     const uint32_t tmem = *taddr_slot;
     bool issued_any = false;
 
+    const uint32_t el = elect_one();
+
     if (warp == 8) {
         // ------------------------------------------------------------ loads
-        if (lane == 0) {
+        if (el) {
             prefetch_tmap(&tm_kv4);
             prefetch_tmap(&tm_kv1);
+            if (rank == 0) desc[cid].n_rows = 0;
         }
-        if (rank == 0 && lane == 0) desc[cid].n_rows = 0;
-        int slot = 0, rslot = 0, issued = 0, rissued = 0;
+        int slot = 0, rslot = 0, n = 0;
         uint32_t ph = 0, rph = 0;
         bool ok = true;
-        // one box of four slabs (columns 64 * z ..) of 64 cache rows from `row`
-        auto push = [&](int row, int z) {
+        const uint32_t full0 = mapa(bar(B_FULL), 0), rfull0 = mapa(bar(B_RFULL), 0);
+        // one box of four slabs (columns 64 * z ..) of 64 cache rows from `row`;
+        // cut: values that are looked through before the MMA reads them
+        auto push = [&](int row, int z, bool cut) {
             if (!ok) return;
-            ok = mbar_wait<true>(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, issued);
+            ok = wait_lanes(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, n);
             if (!ok) return;
-            mbar_arrive_expect_tx(bar(B_FULL + slot), kSlotBytes);
-            tma_load_3d(sbase + kOffRing + slot * kSlotBytes, &tm_kv4, 0, row, z, bar(B_FULL + slot));
-            ++issued;
+            if (el) {
+                const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
+                if (cut) {
+                    mbar_arrive_expect_tx(bar(B_VCUT + slot), kSlotBytes);
+                    tma_load_3d(dst, &tm_kv4, 0, row, z, bar(B_VCUT + slot));
+                    if (rank == 0) mbar_arrive(bar(B_FULL + slot));
+                } else {
+                    if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + slot), 2 * kSlotBytes);
+                    tma_load_3d_pair(dst, &tm_kv4, 0, row, z, full0 + 8u * (uint32_t)slot);
+                }
+            }
+            __syncwarp();
             if (++slot == kSlots) {
                 slot = 0;
                 ph ^= 1u;
@@ -382,7 +414,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         Part p;
         while (ok && walk.next(args, pc, p)) {
             if (p.a >= p.b) continue;
-            if (rank == 0 && lane == 0 && p.b == p.u.nt && p.a > 0) {
+            if (rank == 0 && el && p.b == p.u.nt && p.a > 0) {
                 SplitDesc d;
                 d.t = p.u.t;
                 d.n_rows = p.u.n * args.Hq;
@@ -397,7 +429,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             // cache rows of the tiles' two blocks of 64 keys, sixteen tiles at a
             // time over the lanes (a block behind the last key reads the one before)
             int rows_l = 0, pa = 0, pb = 0;
-            for (int j = p.a; j < p.b; ++j) {
+            bool pcut = false;
+            for (int j = p.a; j < p.b && ok; ++j, ++n) {
                 if (((j - p.a) & 15) == 0) {
                     const int jj = min(j + (lane >> 1), p.b - 1);
                     int s = p.u.key0(jj) + (lane & 1) * 64;
@@ -406,83 +439,37 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 }
                 const int e = ((j - p.a) & 15) * 2;
                 const int ra = __shfl_sync(0xffffffffu, rows_l, e), rb = __shfl_sync(0xffffffffu, rows_l, e + 1);
-                if (lane == 0) {
-                    const int own = rank ? rb : ra;
-                    push(own, 0);
-                    push(own, 4);
-                    if (ok) ok = mbar_wait<true>(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, rissued);
-                    if (ok) {
-                        mbar_arrive_expect_tx(bar(B_RFULL + rslot), kSlab);
-                        tma_load_3d(sbase + kOffRope + rslot * kSlab, &tm_kv1, 0, own, 8, bar(B_RFULL + rslot));
-                        ++rissued;
-                        rslot ^= 1;
-                        if (rslot == 0) rph ^= 1u;
-                    }
-                    if (j > p.a) {
-                        push(pa, 4 * (int)rank);
-                        push(pb, 4 * (int)rank);
-                    }
-                    if (j == p.b - 1) {
-                        push(ra, 4 * (int)rank);
-                        push(rb, 4 * (int)rank);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                const bool cut = !p.u.all_see(p.u.key0(j), kTile);
+                const int own = rank ? rb : ra;
+                push(own, 0, false);
+                push(own, 4, false);
+                if (ok) ok = wait_lanes(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, n);
                 if (!ok) break;
+                if (el) {
+                    if (rank == 0) mbar_arrive_expect_tx(bar(B_RFULL + rslot), 2 * kSlab);
+                    tma_load_3d_pair(sbase + kOffRope + rslot * kSlab, &tm_kv1, 0, own, 8, rfull0 + 8u * (uint32_t)rslot);
+                }
+                __syncwarp();
+                rslot ^= 1;
+                if (rslot == 0) rph ^= 1u;
+                const int z = 4 * (int)rank;
+                if (j > p.a) {
+                    push(pa, z, pcut);
+                    push(pb, z, pcut);
+                }
+                if (j == p.b - 1) {
+                    push(ra, z, cut);
+                    push(rb, z, cut);
+                }
                 pa = ra;
                 pb = rb;
+                pcut = cut;
             }
         }
-        if (!ok && lane == 0) {
-            // copies in flight land before the CTA gives its shared memory up
+        if (!ok) {
+            // given up: copies in flight land before the CTA gives its shared memory up
             const uint64_t t0 = globaltimer_ns();
-            for (int i = max(0, issued - kSlots); i < issued; ++i)
-                while (!mbar_try_wait(bar(B_FULL + i % kSlots), (i / kSlots) & 1) &&
-                       globaltimer_ns() - t0 < kWaitLimitNs) {
-                }
-            for (int i = max(0, rissued - 2); i < rissued; ++i)
-                while (!mbar_try_wait(bar(B_RFULL + (i & 1)), (i >> 1) & 1) &&
-                       globaltimer_ns() - t0 < kWaitLimitNs) {
-                }
-        }
-    } else if (warp == 10 && rank == 1) {
-        // ------------------------------- "loaded" signals of the odd CTA, passed on
-        int slot = 0, rslot = 0, n = 0;
-        uint32_t ph = 0, rph = 0;
-        bool ok = true;
-        auto pass = [&]() {
-            if (!ok) return;
-            ok = mbar_wait<true>(bar(B_FULL + slot), ph, abort_flag, 1100 + slot, n);
-            if (!ok) return;
-            mbar_arrive_cluster(mapa(bar(B_PEER + slot), 0));
-            if (++slot == kSlots) {
-                slot = 0;
-                ph ^= 1u;
-            }
-        };
-        Walk walk(pc);
-        Part p;
-        while (ok && walk.next(args, pc, p)) {
-            for (int j = p.a; j < p.b && ok; ++j, ++n) {
-                if (lane == 0) {
-                    pass();
-                    pass();
-                    if (ok) ok = mbar_wait<true>(bar(B_RFULL + rslot), rph, abort_flag, 1110 + rslot, n);
-                    if (ok) {
-                        mbar_arrive_cluster(mapa(bar(B_RPEER + rslot), 0));
-                        rslot ^= 1;
-                        if (rslot == 0) rph ^= 1u;
-                    }
-                    if (j > p.a) {
-                        pass();
-                        pass();
-                    }
-                    if (j == p.b - 1) {
-                        pass();
-                        pass();
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            while (globaltimer_ns() - t0 < 200000ull) {
             }
         }
     } else if (warp == 9 && rank == 0) {
@@ -496,60 +483,55 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         int slot = 0, rslot = 0, g = 0, n_units = 0;
         uint32_t ph = 0, rph = 0;
         bool ok = true;
-        auto loaded = [&]() -> bool {
-            return mbar_wait<true>(bar(B_FULL + slot), ph, abort_flag, 1200 + slot, g) &&
-                   mbar_wait<true>(bar(B_PEER + slot), ph, abort_flag, 1210 + slot, g);
+        // lane 0 waits for the slot, lane 1 for another barrier (par > 1: none)
+        auto ready = [&](int other, uint32_t par, int tag) -> bool {
+            const bool two = lane == 1 && par <= 1u;
+            return wait_lanes(two ? bar(other) : bar(B_FULL + slot), two ? par : ph, abort_flag, tag, g);
         };
         auto done = [&]() {
-            mma_commit_pair(bar(B_EMPTY + slot));
+            mma_commit_pair(bar(B_EMPTY + slot), el);
             if (++slot == kSlots) {
                 slot = 0;
                 ph ^= 1u;
             }
         };
-        // S = Q C^T of tile g
+        // S = Q C^T of tile g, once the softmax has read the last S
         auto qk = [&]() -> bool {
-            if (g > 0 && !mbar_wait<true>(bar(B_SFREE), (g - 1) & 1, abort_flag, 1220, g)) return false;
-            if (!loaded()) return false;
+            if (!ready(B_SFREE, g > 0 ? (uint32_t)((g - 1) & 1) : 2u, 1220)) return false;
             tc_fence_after();
             uint64_t b = d_k + (uint64_t)(slot * (kSlotBytes >> 4));
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk)
                 mma_pair_ts(tmem + kColS, tmem + kColQ + kk * 8, b + (kk >> 2) * (kSlab >> 4) + (kk & 3) * 2, id_qk,
-                            kk > 0 ? 1u : 0u);
+                            kk > 0 ? 1u : 0u, el);
             done();
-            if (!loaded()) return false;
+            if (!ready(B_RFULL + rslot, rph, 1230)) return false;
             tc_fence_after();
             b = d_k + (uint64_t)(slot * (kSlotBytes >> 4));
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk) {
                 const uint64_t bk = b + (kk >> 2) * (kSlab >> 4) + (kk & 3) * 2;
                 if (kk < 8)
-                    mma_pair_ts(tmem + kColS, tmem + kColQ + (16 + kk) * 8, bk, id_qk, 1u);
+                    mma_pair_ts(tmem + kColS, tmem + kColQ + (16 + kk) * 8, bk, id_qk, 1u, el);
                 else
-                    mma_pair_ss(tmem + kColS, d_q + ((kk - 8) >> 2) * (kSlab >> 4) + (kk & 3) * 2, bk, id_qk, 1u);
+                    mma_pair_ss(tmem + kColS, d_q + ((kk - 8) >> 2) * (kSlab >> 4) + (kk & 3) * 2, bk, id_qk, 1u, el);
             }
             done();
-            if (!mbar_wait<true>(bar(B_RFULL + rslot), rph, abort_flag, 1230, g) ||
-                !mbar_wait<true>(bar(B_RPEER + rslot), rph, abort_flag, 1231, g))
-                return false;
-            tc_fence_after();
             b = d_r + (uint64_t)(rslot * (kSlab >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_pair_ss(tmem + kColS, d_q + 2 * (kSlab >> 4) + kk * 2, b + kk * 2, id_qk, 1u);
-            mma_commit_pair(bar(B_REMPTY + rslot));
+                mma_pair_ss(tmem + kColS, d_q + 2 * (kSlab >> 4) + kk * 2, b + kk * 2, id_qk, 1u, el);
+            mma_commit_pair(bar(B_REMPTY + rslot), el);
             rslot ^= 1;
             if (rslot == 0) rph ^= 1u;
-            mma_commit_pair(bar(B_SFULL));
+            mma_commit_pair(bar(B_SFULL), el);
             return true;
         };
         // O (+)= P C[:, 0:512] of tile gp
         auto pv = [&](int gp, bool first) -> bool {
-            if (!mbar_wait<true>(bar(B_PFULL), gp & 1, abort_flag, 1240, gp)) return false;
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
-                if (!loaded()) return false;
+                if (!ready(B_PFULL, blk == 0 ? (uint32_t)(gp & 1) : 2u, 1240)) return false;
                 tc_fence_after();
                 const uint64_t b = d_v + (uint64_t)(slot * (kSlotBytes >> 4));
 #pragma unroll
@@ -558,29 +540,26 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                     for (int kk = 0; kk < 4; ++kk)
                         mma_pair_ss(tmem + kColO + n * 128, d_p + blk * (kSlab >> 4) + kk * 2,
                                     b + n * (2 * kSlab >> 4) + kk * (16 * 128 >> 4), id_pv,
-                                    first && blk == 0 && kk == 0 ? 0u : 1u);
+                                    first && blk == 0 && kk == 0 ? 0u : 1u, el);
                 done();
             }
-            mma_commit_pair(bar(B_PVDONE));
+            mma_commit_pair(bar(B_PVDONE), el);
             return true;
         };
         Walk walk(pc);
         Part p;
         while (ok && walk.next(args, pc, p)) {
             if (p.a >= p.b) continue;
-            if (lane == 0) {
-                ok = mbar_wait<true>(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
-                const int nt = p.b - p.a;
-                for (int j = 0; j < nt && ok; ++j) {
-                    ok = qk();
-                    issued_any = true;
-                    ++g;
-                    if (ok && j > 0) ok = pv(g - 2, j == 1);
-                }
-                if (ok) ok = pv(g - 1, nt == 1);
+            ok = wait_lanes(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
+            const int nt = p.b - p.a;
+            for (int j = 0; j < nt && ok; ++j) {
+                ok = qk();
+                issued_any = true;
+                ++g;
+                if (ok && j > 0) ok = pv(g - 2, j == 1);
             }
+            if (ok) ok = pv(g - 1, nt == 1);
             ++n_units;
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
     } else if (warp < 8) {
         // ----------------------------------------- softmax, Q, epilogue
@@ -652,6 +631,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         bool have = advance(cur);
         if (have) write_q(cur.u.t);
         int g = 0, ring = 0, uc = 0;
+        uint32_t cut_ph = 0;      // phase of each slot's VCUT
         while (have && ok) {
             const Unit& u = cur.u;
             const int nt = cur.b - cur.a;
@@ -685,7 +665,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(sfree0);
+                    // the loads' results are here, so the signal need not order them
+                    if (lane == 0) mbar_arrive_remote_relaxed(sfree0);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(sr[e]) * scale_log2;
                 }
@@ -757,7 +738,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
 #pragma unroll 1
                     for (int blk = 0; blk < 2; ++blk) {
                         const int rs = (v0 + blk) % kSlots;
-                        if (!wait_all(bar(B_FULL + rs), ((v0 + blk) / kSlots) & 1, abort_flag, 1330, g)) { ok = false; break; }
+                        if (!wait_all(bar(B_VCUT + rs), (cut_ph >> rs) & 1u, abort_flag, 1330, g)) { ok = false; break; }
+                        cut_ph ^= 1u << rs;
                         uint8_t* slab = sgen + kOffRing + rs * kSlotBytes;
                         const int row = (threadIdx.x >> 3) & 31;
 #pragma unroll 1
@@ -838,9 +820,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         }
     }
 
-    if (warp == 9 && lane == 0 && issued_any) {
+    if (warp == 9 && issued_any) {
         // every MMA issued completes before TMEM is released
-        mma_commit_pair(bar(B_DRAIN));
+        mma_commit_pair(bar(B_DRAIN), el);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(bar(B_DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
