@@ -18,8 +18,8 @@
 // CTA); box loads of 24 to 32 KB reach 85 B/clk/SM from L2 and 7.4 TB/s from
 // HBM, single 8 KB ones 22 B/clk, so a tile is loaded in boxes of four slabs of
 // 64 columns x 64 keys, through one ring in the order the MMAs consume:
-//   K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1)
-// While the softmax of tile j runs, the tensor pipe does PV(j-1) and QK(j+1).
+//   Q K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1)
+// so a unit's Q is on its way while the unit before it ends. While the softmax of tile j runs, the tensor pipe does PV(j-1) and QK(j+1).
 //
 // Work is split evenly over the clusters: the units' tiles lie on one line
 // (with a constant per unit for its Q and its epilogue) that is cut into equal
@@ -58,18 +58,20 @@ constexpr int kOffRing = kOffRope + 2 * kSlab;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
 constexpr int kOffRed = kOffBar + 512;                // [2][4][64] row maxima
 constexpr int kOffLsum = kOffRed + 2 * 4 * 64 * 4;    // [2][4][64] row sums
-constexpr int kOffPlan = kOffLsum + 2 * 4 * 64 * 4;
+constexpr int kOffBad = kOffLsum + 2 * 4 * 64 * 4;    // [2][8] flags of the softmax warps
+constexpr int kOffPlan = kOffBad + 64;
 constexpr int kTcSmem = kOffPlan + 256 + 1024;        // + alignment slack
 static_assert(kTcSmem <= 232448, "shared memory");
 
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
 // On the even CTA's barriers: FULL, RFULL (bytes of both CTAs), QT, SFREE, PFULL
-// (arrivals of both). VCUT: a slot with values of a tile that not every row
-// sees whole, on each CTA's own.
+// (arrivals of both). OWN: a slot that the softmax warps look at first (a unit's
+// Q, the values of a tile that not every row sees whole), QROPE: Q's last
+// slab, on each CTA's own.
 enum : int {
-    B_FULL = 0, B_EMPTY = 5, B_VCUT = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
-    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_COUNT = 28
+    B_FULL = 0, B_EMPTY = 5, B_OWN = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
+    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QROPE = 28, B_COUNT = 29
 };
 
 constexpr int kMaxClusters = 74;
@@ -86,7 +88,8 @@ struct SplitDesc {
     int ncl, pad;
 };
 
-// Workspace: [2 parts per cluster][128][512] fp32, their log2 sums, descriptors.
+// Workspace: [2 parts per cluster][512 / 4 columns][128 rows][4] fp32 (a warp's
+// lanes hold rows), their log2 sums, descriptors.
 constexpr size_t kPartBytes = (size_t)kMaxClusters * 2 * kRows * kDv * 4;
 constexpr size_t kPartLseBytes = (size_t)kMaxClusters * 2 * kRows * 4;
 constexpr size_t kWsBytes = kPartBytes + kPartLseBytes + kMaxClusters * sizeof(SplitDesc);
@@ -191,6 +194,7 @@ __device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
     const int per = ceil_div(a.T, kTcThreads);
     const int r0 = min(a.T, tid * per), r1 = min(a.T, r0 + per);
     auto breaks = [&](int t) { return t == 0 || a.pg.seq[t] != a.pg.seq[t - 1]; };
+    if (r0 < r1) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.pos + r0));
     // start of the run that row r0 lies in: the last break before or at it
     int last = -1;
     for (int t = r0; t < r1; ++t)
@@ -323,7 +327,8 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __grid_constant__ CUtensorMap tm_kv1,
-                         const __nv_bfloat16* __restrict__ q, const Args args, float scale_log2,
+                         const __grid_constant__ CUtensorMap tm_q4, const __grid_constant__ CUtensorMap tm_q1,
+                         const Args args, float scale_log2,
                          __nv_bfloat16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
                          float* __restrict__ part_lse, SplitDesc* __restrict__ desc)
 {
@@ -343,7 +348,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(bar(B_FULL + s), 1);
             mbar_init(bar(B_EMPTY + s), 1);
-            mbar_init(bar(B_VCUT + s), 1);
+            mbar_init(bar(B_OWN + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(B_RFULL + b), 1);
@@ -358,6 +363,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         mbar_init(bar(B_PVDONE), 1);
         mbar_init(bar(B_LSUM), 8);
         mbar_init(bar(B_DRAIN), 1);
+        mbar_init(bar(B_QROPE), 1);
         *abort_flag = 0;
         fence_mbar_init_cluster();
     }
@@ -381,6 +387,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         if (el) {
             prefetch_tmap(&tm_kv4);
             prefetch_tmap(&tm_kv1);
+            prefetch_tmap(&tm_q4);
+            prefetch_tmap(&tm_q1);
             if (rank == 0) desc[cid].n_rows = 0;
         }
         int slot = 0, rslot = 0, n = 0;
@@ -388,20 +396,20 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         bool ok = true;
         const uint32_t full0 = mapa(bar(B_FULL), 0), rfull0 = mapa(bar(B_RFULL), 0);
         // one box of four slabs (columns 64 * z ..) of 64 cache rows from `row`;
-        // cut: values that are looked through before the MMA reads them
-        auto push = [&](int row, int z, bool cut) {
+        // for own, the softmax warps wait for it and the MMA for them
+        auto push = [&](const CUtensorMap* tm, int row, int z, bool own) {
             if (!ok) return;
             ok = wait_lanes(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, n);
             if (!ok) return;
             if (el) {
                 const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
-                if (cut) {
-                    mbar_arrive_expect_tx(bar(B_VCUT + slot), kSlotBytes);
-                    tma_load_3d(dst, &tm_kv4, 0, row, z, bar(B_VCUT + slot));
+                if (own) {
+                    mbar_arrive_expect_tx(bar(B_OWN + slot), kSlotBytes);
+                    tma_load_3d(dst, tm, 0, row, z, bar(B_OWN + slot));
                     if (rank == 0) mbar_arrive(bar(B_FULL + slot));
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + slot), 2 * kSlotBytes);
-                    tma_load_3d_pair(dst, &tm_kv4, 0, row, z, full0 + 8u * (uint32_t)slot);
+                    tma_load_3d_pair(dst, tm, 0, row, z, full0 + 8u * (uint32_t)slot);
                 }
             }
             __syncwarp();
@@ -410,10 +418,35 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 ph ^= 1u;
             }
         };
+        // the last slab (the rope columns)
+        auto push_rope = [&](const CUtensorMap* tm, int row, bool own) {
+            if (!ok) return;
+            ok = wait_lanes(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, n);
+            if (!ok) return;
+            if (el) {
+                const uint32_t dst = sbase + kOffRope + rslot * kSlab;
+                if (own) {
+                    mbar_arrive_expect_tx(bar(B_QROPE), kSlab);
+                    tma_load_3d(dst, tm, 0, row, 8, bar(B_QROPE));
+                    if (rank == 0) mbar_arrive(bar(B_RFULL + rslot));
+                } else {
+                    if (rank == 0) mbar_arrive_expect_tx(bar(B_RFULL + rslot), 2 * kSlab);
+                    tma_load_3d_pair(dst, tm, 0, row, 8, rfull0 + 8u * (uint32_t)rslot);
+                }
+            }
+            __syncwarp();
+            rslot ^= 1;
+            if (rslot == 0) rph ^= 1u;
+        };
         Walk walk(pc);
         Part p;
         while (ok && walk.next(args, pc, p)) {
             if (p.a >= p.b) continue;
+            // this CTA's 64 of the unit's pairs (rows behind the last are read as zeros)
+            const int qrow = p.u.t * args.Hq + (int)rank * 64;
+            push(&tm_q4, qrow, 0, true);
+            push(&tm_q4, qrow, 4, true);
+            push_rope(&tm_q1, qrow, true);
             if (rank == 0 && el && p.b == p.u.nt && p.a > 0) {
                 SplitDesc d;
                 d.t = p.u.t;
@@ -441,25 +474,17 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 const int ra = __shfl_sync(0xffffffffu, rows_l, e), rb = __shfl_sync(0xffffffffu, rows_l, e + 1);
                 const bool cut = !p.u.all_see(p.u.key0(j), kTile);
                 const int own = rank ? rb : ra;
-                push(own, 0, false);
-                push(own, 4, false);
-                if (ok) ok = wait_lanes(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, n);
-                if (!ok) break;
-                if (el) {
-                    if (rank == 0) mbar_arrive_expect_tx(bar(B_RFULL + rslot), 2 * kSlab);
-                    tma_load_3d_pair(sbase + kOffRope + rslot * kSlab, &tm_kv1, 0, own, 8, rfull0 + 8u * (uint32_t)rslot);
-                }
-                __syncwarp();
-                rslot ^= 1;
-                if (rslot == 0) rph ^= 1u;
+                push(&tm_kv4, own, 0, false);
+                push(&tm_kv4, own, 4, false);
+                push_rope(&tm_kv1, own, false);
                 const int z = 4 * (int)rank;
                 if (j > p.a) {
-                    push(pa, z, pcut);
-                    push(pb, z, pcut);
+                    push(&tm_kv4, pa, z, pcut);
+                    push(&tm_kv4, pb, z, pcut);
                 }
                 if (j == p.b - 1) {
-                    push(ra, z, cut);
-                    push(rb, z, cut);
+                    push(&tm_kv4, ra, z, cut);
+                    push(&tm_kv4, rb, z, cut);
                 }
                 pa = ra;
                 pb = rb;
@@ -551,6 +576,12 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         while (ok && walk.next(args, pc, p)) {
             if (p.a >= p.b) continue;
             ok = wait_lanes(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
+            // the softmax warps have taken Q out of its two slots and rope slot
+            done();
+            done();
+            mma_commit_pair(bar(B_REMPTY + rslot), el);
+            rslot ^= 1;
+            if (rslot == 0) rph ^= 1u;
             const int nt = p.b - p.a;
             for (int j = 0; j < nt && ok; ++j) {
                 ok = qk();
@@ -574,52 +605,56 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         const int grp = side * 2 + hs;
         float* red = reinterpret_cast<float*>(sgen + kOffRed);
         float* lsum_s = reinterpret_cast<float*>(sgen + kOffLsum);
+        int* bad_s = reinterpret_cast<int*>(sgen + kOffBad);
         const uint32_t qt0 = mapa(bar(B_QT), 0), sfree0 = mapa(bar(B_SFREE), 0), pfull0 = mapa(bar(B_PFULL), 0);
-        const size_t all_rows = (size_t)args.T * args.Hq;
         bool ok = true;
-        // Q of a unit: columns [0, 384) to TMEM (row i % 64 in both lanes), the
-        // others to shared memory
-        auto write_q = [&](int t) {
-            const size_t row0 = (size_t)t * args.Hq;
-            const uint4* src = reinterpret_cast<const uint4*>(q + min(row0 + r, all_rows - 1) * kDqk + 192 * hs);
-            uint4 tail[6];
-#pragma unroll
-            for (int it = 0; it < 6; ++it) {
-                const int p = it * 256 + (int)threadIdx.x;
-                tail[it] = __ldg(reinterpret_cast<const uint4*>(
-                                     q + min(row0 + rank * 64 + p / 24, all_rows - 1) * kDqk + 384) + p % 24);
-            }
+        int ring = 0, rope = 0;   // ring places passed by this unit and those before
+        uint32_t own_ph = 0;      // phase of each slot's OWN
+        auto own_slot = [&](int place) -> int {
+            const int rs = place % kSlots;
+            if (!wait_all(bar(B_OWN + rs), (own_ph >> rs) & 1u, abort_flag, 1330 + rs, place)) return -1;
+            own_ph ^= 1u << rs;
+            return rs;
+        };
+        // Q of the unit at ring place `ring`: columns [0, 384) go to TMEM (row
+        // i % 64 in both lanes), the others to their place in shared memory
+        auto write_q = [&](int units) -> bool {
+            const int s0 = own_slot(ring), s1 = own_slot(ring + 1);
+            if (s0 < 0 || s1 < 0 || !wait_all(bar(B_QROPE), units & 1, abort_flag, 1336, units)) return false;
+            const uint32_t q0 = sbase + kOffRing + s0 * kSlotBytes, q1 = sbase + kOffRing + s1 * kSlotBytes;
 #pragma unroll
             for (int b = 0; b < 3; ++b) {
+                const int sl = 3 * hs + b;
+                const uint32_t src = (sl < 4 ? q0 + sl * kSlab : q1 + (sl - 4) * kSlab) + lr * 128;
                 uint32_t w[32];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) {
-                    const uint4 x = __ldg(src + 8 * b + v);
+                    const uint4 x = ld_shared_v4(src + ((v ^ (lr & 7)) << 4));
                     w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
                 }
-                tmem_st32(tmem + lane_addr + kColQ + 96 * hs + 32 * b, w);
+                tmem_st32(tmem + lane_addr + kColQ + 32 * sl, w);
             }
 #pragma unroll
             for (int it = 0; it < 6; ++it) {
-                const int p = it * 256 + (int)threadIdx.x, row = p / 24, c = p % 24;
-                st_shared_v4(sbase + kOffQ + (c >> 3) * kSlab + row * 128 + (((c & 7) ^ (row & 7)) << 4), tail[it]);
+                const uint32_t o = (uint32_t)(it & 1) * 4096 + threadIdx.x * 16;
+                const uint32_t src = it < 4 ? q1 + (2 + (it >> 1)) * kSlab : sbase + kOffRope + (rope & 1) * kSlab;
+                st_shared_v4(sbase + kOffQ + (it >> 1) * kSlab + o, ld_shared_v4(src + o));
             }
             tmem_wait_st();
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(qt0);
+            return true;
         };
-        auto out_row = [&](const Unit& u) {
-            return out + ((size_t)u.t * args.Hq + r) * kDv + side * 256 + 128 * hs;
-        };
+        const int col0 = side * 256 + 128 * hs;             // output columns of this warp
         // the next part with keys; units without any are written on the way
         Walk walk(pc);
         auto advance = [&](Part& p) -> bool {
             while (walk.next(args, pc, p)) {
                 if (p.a < p.b) return true;
                 if (r < p.u.n * args.Hq) {
-                    uint4* dst = reinterpret_cast<uint4*>(out_row(p.u));
+                    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)p.u.t * args.Hq + r) * kDv + col0);
                     for (int v = 0; v < 16; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
                     if (grp == 0) lse[(size_t)p.u.t * args.Hq + r] = -INFINITY;
                 }
@@ -629,9 +664,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         };
         Part cur, nxt;
         bool have = advance(cur);
-        if (have) write_q(cur.u.t);
-        int g = 0, ring = 0, uc = 0;
-        uint32_t cut_ph = 0;      // phase of each slot's VCUT
+        if (have) ok = write_q(0);
+        int g = 0, uc = 0;
         while (have && ok) {
             const Unit& u = cur.u;
             const int nt = cur.b - cur.a;
@@ -647,11 +681,6 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 if (n > 0) vis = visible_of(n, args.pos[t], args.window, args.sinks);
             }
             const bool more = advance(nxt);
-            if (more) {
-                const char* qn = reinterpret_cast<const char*>(q + min((size_t)nxt.u.t * args.Hq + r, all_rows - 1) * kDqk);
-                for (int o = grp * 128; o < kDqk * 2; o += 512)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(qn + o));
-            }
             float m_use = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++g) {
                 const int key0 = u.key0(cur.a + j);
@@ -671,10 +700,23 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                     for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(sr[e]) * scale_log2;
                 }
                 if (!whole) {
-                    const uint32_t bits = seen_bits(vis, key0 + 64 * side + 32 * hs);
+                    // -inf for a key that the row does not see; a note if the logit of a
+                    // key that some row does not see is no number (then neither is
+                    // one of its columns: any row tells, in both CTAs alike)
+                    const int s0 = key0 + 64 * side + 32 * hs;
+                    Visible every;
+                    every.lo = u.max_lo;
+                    every.hi = u.min_hi;
+                    every.sink_end = u.sink_end;
+                    const uint32_t bits = seen_bits(vis, s0), all = seen_bits(every, s0);
+                    bool bad = false;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 32; ++e) {
+                        if (!((all >> e) & 1u)) bad |= !(fabsf(x[e]) < INFINITY);
                         if (!((bits >> e) & 1u)) x[e] = -INFINITY;
+                    }
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (lane == 0) bad_s[(g & 1) * 8 + warp] = bad ? 1 : 0;
                 }
                 float mx[16];
 #pragma unroll
@@ -734,24 +776,25 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                                  make_uint4(pk[4 * m], pk[4 * m + 1], pk[4 * m + 2], pk[4 * m + 3]));
                 if (!whole) {
                     // ring places of this tile's values: behind the next tile's keys
-                    const int v0 = ring + 4 * j + (j < nt - 1 ? 4 : 2);
+                    const int v0 = ring + 2 + 4 * j + (j < nt - 1 ? 4 : 2);
+                    int bad = 0;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) bad |= bad_s[(g & 1) * 8 + w];
 #pragma unroll 1
-                    for (int blk = 0; blk < 2; ++blk) {
-                        const int rs = (v0 + blk) % kSlots;
-                        if (!wait_all(bar(B_VCUT + rs), (cut_ph >> rs) & 1u, abort_flag, 1330, g)) { ok = false; break; }
-                        cut_ph ^= 1u << rs;
+                    for (int blk = 0; blk < 2 && ok; ++blk) {
+                        const int rs = own_slot(v0 + blk);
+                        ok = rs >= 0;
+                        if (!bad || !ok) continue;
                         uint8_t* slab = sgen + kOffRing + rs * kSlotBytes;
-                        const int row = (threadIdx.x >> 3) & 31;
 #pragma unroll 1
-                        for (int rr = row; rr < 64; rr += 32) {
+                        for (int rr = (int)threadIdx.x >> 3; rr < 64; rr += 32) {
                             if (u.all_see(key0 + 64 * blk + rr, 1)) continue;
 #pragma unroll
                             for (int sl = 0; sl < 4; ++sl) {
                                 uint4* v = reinterpret_cast<uint4*>(slab + sl * kSlab + rr * 128) + (threadIdx.x & 7);
                                 const uint4 w = *v;
-                                const uint4 c = make_uint4(finite_halves(w.x), finite_halves(w.y), finite_halves(w.z),
-                                                           finite_halves(w.w));
-                                if (c.x != w.x || c.y != w.y || c.z != w.z || c.w != w.w) *v = c;
+                                *v = make_uint4(finite_halves(w.x), finite_halves(w.y), finite_halves(w.z),
+                                                finite_halves(w.w));
                             }
                         }
                     }
@@ -761,10 +804,11 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(pfull0);
             }
-            ring += 4 * nt;
+            ring += 2 + 4 * nt;
+            rope += 1 + nt;
             if (!ok) break;
             // every QK of this unit has completed: Q makes room for the next unit's
-            if (more) write_q(nxt.u.t);
+            if (more && !write_q(uc + 1)) { ok = false; break; }
             // row sum over the four threads of the row
             lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
             __syncwarp();
@@ -778,21 +822,24 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             const float lv = l != 0.f ? m_use + __log2f(l) : -INFINITY;
             const bool split = cur.split();
             const size_t prow = ((size_t)cid * 2 + (cur.start < pc.w0 ? 0 : 1)) * kRows + r;
-            float* po = part_o + prow * kDv + side * 256 + 128 * hs;
-            __nv_bfloat16* orow = out_row(u);
+            float4* po = reinterpret_cast<float4*>(part_o) + (prow - r) * (kDv / 4) + r;
+            // rows leave through the shared memory of this warp's P, 64 bytes each at
+            // a time, so that stores cover whole sectors
+            const uint32_t stage = sbase + kOffP + side * kSlab;
 #pragma unroll 1
             for (int q4 = 0; q4 < 4; ++q4) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_addr + kColO + 128 * hs + q4 * 32, o);
                 tmem_wait_ld();
-                if (live && split) {
-                    float4* dst = reinterpret_cast<float4*>(po + q4 * 32);
+                if (split) {
+                    if (live) {
 #pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                             __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-                } else if (live) {
-                    uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
+                        for (int v = 0; v < 8; ++v)
+                            po[(size_t)(col0 / 4 + q4 * 8 + v) * kRows] =
+                                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+                    }
+                } else {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint32_t w[4];
@@ -800,7 +847,16 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]) * inv,
                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-                        dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+                        st_shared_v4(stage + lr * 128 + (((4 * hs + v) ^ (lr & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int row = (lr & 32) + it * 8 + (lane >> 2), v = lane & 3;
+                        const uint4 w = ld_shared_v4(stage + row * 128 + (((4 * hs + v) ^ (row & 7)) << 4));
+                        const int rr = (int)rank * 64 + row;
+                        if (rr < u.n * args.Hq)
+                            *reinterpret_cast<uint4*>(out + ((size_t)u.t * args.Hq + rr) * kDv + col0 + q4 * 32 + v * 8) = w;
                     }
                 }
                 __syncwarp();
@@ -838,61 +894,74 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
 
 // Joins the parts of a split unit, in the order of the clusters:
 //   lse = log sum_z 2^lse_z,  out = sum_z 2^(lse_z - lse) o_z.
-// One CTA per (cluster that ended a split unit, 8 of its pairs).
-constexpr int kJoinRows = 8;
+// One CTA per (cluster that ended a split unit, 4 of its pairs); its CTAs for
+// clusters that ended none leave at once.
+constexpr int kJoinRows = 4;
+constexpr int kJoinThreads = 256;
 
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                            const SplitDesc* __restrict__ desc, int Hq, __nv_bfloat16* __restrict__ out,
                            float* __restrict__ lse)
 {
-    __shared__ float wz[kJoinRows][kMaxClusters];
+    __shared__ float wz[kMaxClusters][kJoinRows];
     __shared__ int where[kMaxClusters];
     griddep_wait();
     const SplitDesc d = desc[blockIdx.x];
     const int r0 = blockIdx.y * kJoinRows;
     if (d.n_rows <= r0) return;
     const int parts = d.c_last - d.c_first + 1;
-    for (int z = threadIdx.x; z < parts; z += 128) {
-        const int c = d.c_first + z;
-        where[z] = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < kJoinRows && r0 + threadIdx.x < d.n_rows) {
-        const int r = r0 + threadIdx.x;
-        float m = -INFINITY;
-        for (int z = 0; z < parts; ++z) {
-            const float v = part_lse[where[z] * kRows + r];
-            wz[threadIdx.x][z] = v;
-            m = fmaxf(m, v);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < kJoinRows) {
+        // a warp per row, lanes over the parts
+        const int r = r0 + warp;
+        float v[3], m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int z = lane + 32 * i;
+            v[i] = -INFINITY;
+            if (z >= parts) continue;
+            const int c = d.c_first + z;
+            const int at = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
+            if (warp == 0) where[z] = at;
+            if (r < d.n_rows) v[i] = part_lse[at * kRows + r];
+            m = fmaxf(m, v[i]);
         }
-        float l = 0.f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float ms = m == -INFINITY ? 0.f : m;
-        for (int z = 0; z < parts; ++z) l += exp2f(wz[threadIdx.x][z] - ms);
+        float l = (exp2f(v[0] - ms) + exp2f(v[1] - ms)) + exp2f(v[2] - ms);
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const float total = l != 0.f ? ms + log2f(l) : -INFINITY;
-        for (int z = 0; z < parts; ++z) {
-            const float v = wz[threadIdx.x][z];
-            wz[threadIdx.x][z] = v == -INFINITY ? 0.f : exp2f(v - total);
-        }
-        lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (lane + 32 * i < parts) wz[lane + 32 * i][warp] = v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
+        if (lane == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < kJoinRows * kDv / 4; e += 128) {
-        const int rr = e / (kDv / 4), c4 = e % (kDv / 4);
-        if (r0 + rr >= d.n_rows) break;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int z = 0; z < parts; ++z) {
-            const float w = wz[rr][z];
-            const float4 v = reinterpret_cast<const float4*>(part_o + ((size_t)where[z] * kRows + r0 + rr) * kDv)[c4];
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+    // 4 rows x 128 groups of four columns, two per thread
+    const int rr = threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
+    constexpr int kStep = kJoinThreads / kJoinRows;
+    if (r0 + rr >= d.n_rows) return;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int z = 0; z < parts; ++z) {
+        const float w = wz[z][rr];
+        const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)where[z] * kRows * (kDv / 4) + r0 + rr;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = p[(size_t)(c4 + i * kStep) * kRows];
+            acc[i].x = fmaf(w, v.x, acc[i].x);
+            acc[i].y = fmaf(w, v.y, acc[i].y);
+            acc[i].z = fmaf(w, v.z, acc[i].z);
+            acc[i].w = fmaf(w, v.w, acc[i].w);
         }
-        reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4] =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4 + i * kStep] =
+            make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
 }
+static_assert(kMaxClusters <= 96 && kDv / 4 == 2 * kJoinThreads / kJoinRows, "the join's lanes and threads");
 
 }  // namespace cache_attn
 }  // namespace dsa

@@ -1224,10 +1224,12 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     if (need && (!workspace || ws_bytes < need || !al16(workspace)))
         return fail(DSA_ERR_WORKSPACE, "paged attention needs %zu workspace bytes (got %zu)", need, ws_bytes);
     const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
-    CUtensorMap tm4, tm1;
+    CUtensorMap tm4, tm1, tq4, tq1;
     const uint64_t pool_rows = (uint64_t)num_pages * page_size;
     if (int rc = make_tmap_slabs(&tm4, kv_pages, kDqk / 64, pool_rows, 4)) return rc;
     if (int rc = make_tmap_slabs(&tm1, kv_pages, kDqk / 64, pool_rows, 1)) return rc;
+    if (int rc = make_tmap_slabs(&tq4, q, kDqk / 64, (uint64_t)T * Hq, 4)) return rc;
+    if (int rc = make_tmap_slabs(&tq1, q, kDqk / 64, (uint64_t)T * Hq, 1)) return rc;
     cudaError_t e = cudaFuncSetAttribute(mla_attn_paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kTcSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_attn_paged_tc_kernel)");
@@ -1247,12 +1249,12 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     const long long work = T * (tiles + kUnitCost);
     const int clusters = (int)std::max(1ll, std::min<long long>(work / kMinWork,
                                                                 std::min(kMaxClusters, std::max(1, num_sms() / 2))));
-    launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1,
-               reinterpret_cast<const __nv_bfloat16*>(q), args, scale * 1.4426950408889634f,
+    launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1, tq4,
+               tq1, args, scale * 1.4426950408889634f,
                reinterpret_cast<__nv_bfloat16*>(out), lse, part_o, part_lse, desc);
     DSA_LAUNCH_CHECK("mla_attn_paged_tc_kernel");
     if (clusters > 1) {
-        launch_pdl(mla_attn_paged_join_kernel, dim3(clusters, kRows / kJoinRows), dim3(128), 0, st, part_o, part_lse,
+        launch_pdl(mla_attn_paged_join_kernel, dim3(clusters, kRows / kJoinRows), dim3(kJoinThreads), 0, st, part_o, part_lse,
                    desc, Hq, reinterpret_cast<__nv_bfloat16*>(out), lse);
         DSA_LAUNCH_CHECK("mla_attn_paged_join_kernel");
     }
