@@ -177,14 +177,16 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
  *                        (a row's -inf adds nothing)
  *   mass  fp32 [n_seqs, max_pages * page_size]   ACCUMULATED into; positions
  *                        that no row sees keep their value
- * Every element is added to by one thread, in the order of the rows: results
- * do not vary from run to run. Other arguments and limits as
- * dsa_mla_attn_paged; no workspace. Asynchronous on `stream`.
+ * An element's terms are added in a fixed order: results do not vary from run
+ * to run. Other arguments and limits as dsa_mla_attn_paged. workspace:
+ * dsa_mla_attn_mass_paged_workspace_size(n_seqs) bytes; calls in flight at
+ * once, captured graphs among them, need one each.
  */
+size_t dsa_mla_attn_mass_paged_workspace_size(int n_seqs);
 int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
                             const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
                             const int32_t* pos, const float* lse, int T, int Hq, int d_qk, float scale, int window,
-                            int sinks, float* mass, void* stream);
+                            int sinks, float* mass, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Eviction from a cache by accumulated weight, first half: which positions

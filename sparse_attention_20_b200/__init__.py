@@ -44,7 +44,8 @@ EXPORTS = ("dsa_workspace_size", "dsa_indexer_topk", "dsa_sparse_mla_attn", "dsa
            "dsa_mla_mha_attn", "dsa_partition_prefill_rows", "dsa_partition_decode_seqs",
            "dsa_sparse_mla_attn_split", "dsa_sparse_mla_attn_split_workspace_size", "dsa_debug_build",
            "dsa_debug_counters", "dsa_phase_timing", "dsa_phase_times", "dsa_mla_attn_paged",
-           "dsa_mla_attn_paged_workspace_size", "dsa_mla_attn_mass_paged", "dsa_cache_evict_select",
+           "dsa_mla_attn_paged_workspace_size", "dsa_mla_attn_mass_paged",
+           "dsa_mla_attn_mass_paged_workspace_size", "dsa_cache_evict_select",
            "dsa_cache_compact_paged")
 
 
@@ -107,7 +108,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dsa_mla_attn_paged_workspace_size.restype = Z
         lib.dsa_mla_attn_paged.argtypes = [P, P, I, I, P, I, I, P, P, I, I, I, I, F, I, I, P, P, P, Z, P]
         lib.dsa_mla_attn_paged.restype = I
-        lib.dsa_mla_attn_mass_paged.argtypes = [P, P, I, I, P, I, I, P, P, P, I, I, I, F, I, I, P, P]
+        lib.dsa_mla_attn_mass_paged_workspace_size.argtypes = [I]
+        lib.dsa_mla_attn_mass_paged_workspace_size.restype = Z
+        lib.dsa_mla_attn_mass_paged.argtypes = [P, P, I, I, P, I, I, P, P, P, I, I, I, F, I, I, P, P, Z, P]
         lib.dsa_mla_attn_mass_paged.restype = I
         lib.dsa_cache_evict_select.argtypes = [P, I, P, I, I, I, I, P, P, P]
         lib.dsa_cache_evict_select.restype = I
@@ -167,7 +170,7 @@ def _arg(t: torch.Tensor, name: str, dtype, shape=None, device=None) -> torch.Te
     _dev(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(int(v) for v in shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(int(v) for v in shape)}")
     return t
 
@@ -356,34 +359,26 @@ def sparse_mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, id
     return out, lse
 
 
-class _Launch:
-    """The device and stream of one call: the operands' device is made current
-    (a stream belongs to one), and `stream` defaults to its current stream.
-    Buffers that the call itself allocates are kept from reuse until a
-    caller's other stream is done with them."""
+def _new(shape, dtype, device, stream, zero=False):
+    """A buffer that the call itself allocates: from the pool of the stream that
+    the call runs on, so that its memory is not in other work's hands."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
-    def __init__(self, device, stream):
-        self.device, self.given = device, stream
-        self.guard = None
 
-    def __enter__(self):
-        if self.device.index is not None and self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def keep(self, t):
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
-
-    @property
-    def handle(self):
-        return _stream(self.given)
+def _run(fn, device, stream, *args) -> None:
+    """Call a C entry with the operands' device current (a stream belongs to
+    one) and, as its last argument, `stream` or that device's current one."""
+    if device.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _run(fn, device, stream, *args)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    rc = fn(*args, raw)
+    if rc != DSA_OK:
+        raise DSAError(rc, last_error())
 
 
 def _pages(t, name, cols=None, dtype=None, page_size=0, device=None):
@@ -417,51 +412,57 @@ def alloc_mla_attn_workspace(T: int, Hq: int, device=None) -> torch.Tensor:
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def alloc_mla_mass_workspace(n_seqs: int, device=None) -> torch.Tensor:
+    """Workspace of ``mla_attn_mass_paged`` for n_seqs sequences."""
+    n = int(load_library().dsa_mla_attn_mass_paged_workspace_size(n_seqs))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
 def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: float, d_v: int, window: int = 0,
                    sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
     """(out bf16 [T, Hq, d_v], lse fp32 [T, Hq]) of dense MQA-mode attention of T
     new tokens over a paged latent cache: row t sees the keys s <= pos[t] of
     sequence seq[t], and with window > 0 only the last `window` of them and
-    the first `sinks`. A row without keys gives out = 0, lse = -inf."""
+    the first `sinks`. A row without keys gives out = 0, lse = -inf.
+
+    Buffers not given are allocated on the stream that the call runs on."""
     q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
                                                                                   block_table, seq, pos)
-    with _Launch(dev, stream) as at:
-        if out is None:
-            out = at.keep(torch.empty((T, Hq, d_v), dtype=torch.bfloat16, device=dev))
-        if lse is None:
-            lse = at.keep(torch.empty((T, Hq), dtype=torch.float32, device=dev))
-        if workspace is None:
-            workspace = at.keep(alloc_mla_attn_workspace(T, Hq, dev))
-        out = _arg(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
-        lse = _arg(lse, "lse", torch.float32, (T, Hq), dev)
-        nbytes = _ws(workspace, dev)
-        _check(load_library().dsa_mla_attn_paged(
-            _ptr(q), _ptr(kv_pages), num_pages, page_size, _ptr(block_table), block_table.shape[0],
-            block_table.shape[1], _ptr(seq), _ptr(pos), T, Hq, d_qk, d_v, float(scale), int(window), int(sinks),
-            _ptr(out), _ptr(lse), _ptr(workspace), nbytes, at.handle))
+    lib = load_library()
+    out = _new((T, Hq, d_v), torch.bfloat16, dev, stream) if out is None else \
+        _arg(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
+    lse = _new((T, Hq), torch.float32, dev, stream) if lse is None else \
+        _arg(lse, "lse", torch.float32, (T, Hq), dev)
+    if workspace is None:
+        workspace = _new(max(lib.dsa_mla_attn_paged_workspace_size(T, Hq), 256), torch.uint8, dev, stream)
+    n_seqs, max_pages = block_table.shape
+    _run(lib.dsa_mla_attn_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages, page_size,
+         block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), T, Hq, d_qk, d_v, scale, window,
+         sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
     return out, lse
 
 
 def mla_attn_mass_paged(q, kv_pages, page_size: int, block_table, seq, pos, lse, scale: float, mass=None,
-                        window: int = 0, sinks: int = 0, stream=None):
+                        window: int = 0, sinks: int = 0, workspace=None, stream=None):
     """mass fp32 [n_seqs, max_pages * page_size] += the attention weight (over
     rows and heads) that each cached token receives from these rows.
 
     lse is ``mla_attn_paged``'s for the same rows, window and sinks. mass is
-    accumulated into (a new zeroed tensor when None)."""
+    accumulated into (a new zeroed tensor when None). workspace: see
+    ``alloc_mla_mass_workspace``."""
     q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
                                                                                   block_table, seq, pos)
-    lse = _arg(lse, "lse", torch.float32, (T, Hq), dev)
-    shape = (block_table.shape[0], block_table.shape[1] * page_size)
-    with _Launch(dev, stream) as at:
-        if mass is None:
-            with torch.cuda.stream(at.given):
-                mass = at.keep(torch.zeros(shape, dtype=torch.float32, device=dev))
-        mass = _arg(mass, "mass", torch.float32, shape, dev)
-        _check(load_library().dsa_mla_attn_mass_paged(
-            _ptr(q), _ptr(kv_pages), num_pages, page_size, _ptr(block_table), shape[0], block_table.shape[1],
-            _ptr(seq), _ptr(pos), _ptr(lse), T, Hq, d_qk, float(scale), int(window), int(sinks), _ptr(mass),
-            at.handle))
+    _arg(lse, "lse", torch.float32, (T, Hq), dev)
+    n_seqs, max_pages = block_table.shape
+    shape = (n_seqs, max_pages * page_size)
+    mass = _new(shape, torch.float32, dev, stream, zero=True) if mass is None else \
+        _arg(mass, "mass", torch.float32, shape, dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _new(lib.dsa_mla_attn_mass_paged_workspace_size(n_seqs), torch.uint8, dev, stream)
+    _run(lib.dsa_mla_attn_mass_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages,
+         page_size, block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), lse.data_ptr(), T, Hq,
+         d_qk, scale, window, sinks, mass.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
     return mass
 
 
@@ -476,19 +477,15 @@ def cache_evict_select(mass, seq_len, keep: int, sinks: int = 0, recent: int = 0
     if mass.dtype != torch.float32 or mass.dim() != 2:
         raise TypeError(f"mass must be float32 [n_seqs, max_len], got {mass.dtype} {tuple(mass.shape)}")
     n_seqs, max_len = mass.shape
-    seq_len = _i32(seq_len, "seq_len", (n_seqs,), dev)
+    _arg(seq_len, "seq_len", torch.int32, (n_seqs,), dev)
     if keep <= 0:
         raise ValueError(f"keep = {keep} must be positive")
-    with _Launch(dev, stream) as at:
-        if keep_idx is None:
-            keep_idx = at.keep(torch.empty((n_seqs, keep), dtype=torch.int32, device=dev))
-        if new_len is None:
-            new_len = at.keep(torch.empty(n_seqs, dtype=torch.int32, device=dev))
-        keep_idx = _arg(keep_idx, "keep_idx", torch.int32, (n_seqs, keep), dev)
-        new_len = _arg(new_len, "new_len", torch.int32, (n_seqs,), dev)
-        _check(load_library().dsa_cache_evict_select(_ptr(mass), max_len, _ptr(seq_len), n_seqs, int(keep),
-                                                     int(sinks), int(recent), _ptr(keep_idx), _ptr(new_len),
-                                                     at.handle))
+    keep_idx = _new((n_seqs, keep), torch.int32, dev, stream) if keep_idx is None else \
+        _arg(keep_idx, "keep_idx", torch.int32, (n_seqs, keep), dev)
+    new_len = _new(n_seqs, torch.int32, dev, stream) if new_len is None else \
+        _arg(new_len, "new_len", torch.int32, (n_seqs,), dev)
+    _run(load_library().dsa_cache_evict_select, dev, stream, mass.data_ptr(), max_len, seq_len.data_ptr(), n_seqs,
+         keep, sinks, recent, keep_idx.data_ptr(), new_len.data_ptr())
     return keep_idx, new_len
 
 
@@ -507,7 +504,7 @@ def cache_compact_paged(kv_pages, page_size: int, block_table, keep_idx, new_len
     keep_idx = _dev(keep_idx, "keep_idx", dev)
     if keep_idx.dtype != torch.int32 or keep_idx.dim() != 2 or keep_idx.shape[0] != n_seqs:
         raise TypeError(f"keep_idx must be int32 [{n_seqs}, keep], got {keep_idx.dtype} {tuple(keep_idx.shape)}")
-    new_len = _i32(new_len, "new_len", (n_seqs,), dev)
+    _arg(new_len, "new_len", torch.int32, (n_seqs,), dev)
     k_bytes = 0
     if k_pages is not None:
         k_pages, k_num = _pages(k_pages, "k_pages", page_size=page_size, device=dev)
@@ -515,12 +512,11 @@ def cache_compact_paged(kv_pages, page_size: int, block_table, keep_idx, new_len
             raise ValueError(f"k_pages has {k_num} pages, kv_pages {num_pages}")
         k_bytes = k_pages.shape[1] * k_pages.element_size()
     if mass is not None:
-        mass = _arg(mass, "mass", torch.float32, (n_seqs, max_pages * page_size), dev)
-    with _Launch(dev, stream) as at:
-        _check(load_library().dsa_cache_compact_paged(
-            _ptr(kv_pages), kv_pages.shape[1] * kv_pages.element_size(), _ptr(k_pages), k_bytes, num_pages,
-            page_size, _ptr(block_table), n_seqs, max_pages, _ptr(keep_idx), keep_idx.shape[1], _ptr(new_len),
-            _ptr(mass), at.handle))
+        _arg(mass, "mass", torch.float32, (n_seqs, max_pages * page_size), dev)
+    _run(load_library().dsa_cache_compact_paged, dev, stream, kv_pages.data_ptr(),
+         kv_pages.shape[1] * kv_pages.element_size(), None if k_pages is None else k_pages.data_ptr(), k_bytes,
+         num_pages, page_size, block_table.data_ptr(), n_seqs, max_pages, keep_idx.data_ptr(), keep_idx.shape[1],
+         new_len.data_ptr(), None if mass is None else mass.data_ptr())
 
 
 def sparse_mla_attn(q, kv, idx, scale: float, d_v: int, pos=None, k_base=None, out=None,

@@ -1,0 +1,702 @@
+// The attention weight that each cached token receives (tensor cores):
+//   mass[b,s] += sum over the rows t of sequence b that see s, and heads h, of
+//                exp(x_{t,h,s} - lse[t,h]),  x = scale q[t,h].c_s.
+//
+// Keys are the M side (S^T = C Q^T), so that a key's sum over rows and heads
+// runs along one TMEM lane and needs no exchange between threads. A cluster of
+// two CTAs does a tile of 256 keys (pair MMA, M = 256: 128 keys per CTA) against
+// 256 (row, head) pairs at a time (N = 256, each CTA brings half of them; N =
+// 128 where a step has no more). The tile's keys stay in shared memory (9 slabs
+// of 64 columns, 144 KB) for all of the sequence's rows, Q streams through a
+// ring of 16 KB slots: 32 B per clock and SM from L2 at the tensor pipe's rate.
+// With one row per sequence a slab of keys is free as soon as its MMAs are done
+// and the next tile's is on its way: 144 KB in flight per SM, bound by HBM.
+//
+// The (tile, 256 pairs) steps of all sequences lie on one line that the
+// clusters share evenly; a tile cut by a boundary leaves partial sums that a
+// second kernel adds in order, so results do not depend on timing. Steps none
+// of whose rows sees a key of the tile are passed over.
+//
+// Warps (10 per CTA): 0-7 sums (two per TMEM lane quarter, half of the columns
+// each), 8 loads, 9 MMA issue (even CTA).
+#pragma once
+#include <cuda.h>
+
+#include "cache_attn_tc.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+namespace cache_mass {
+
+using namespace sm100;
+using cache_attn::Args;
+using cache_attn::Visible;
+using cache_attn::visible_of;
+using cache_attn::wait_all;
+using cache_attn::wait_lanes;
+
+constexpr int kDqk = cache_attn::kDqk;
+constexpr int kSlabs = kDqk / 64;
+constexpr int kTile = 256;                 // keys of a tile (both CTAs)
+constexpr int kPairs = 256;                // (row, head) pairs of a step
+constexpr int kThreads = 320;
+constexpr int kKSlab = 128 * 128;          // 128 keys x 64 columns
+constexpr int kQSlot = 128 * 128;          // 128 pairs x 64 columns
+constexpr int kQSlots = 4;
+constexpr int kOffK = 0;
+constexpr int kOffQ = kOffK + kSlabs * kKSlab;
+constexpr int kOffBar = kOffQ + kQSlots * kQSlot;
+constexpr int kOffCol = kOffBar + 512;                    // [2][256] lse2, last and first key seen
+constexpr int kOffHalf = kOffCol + 2 * 3 * kPairs * 4;    // [2][128] sums of the second column half
+constexpr int kOffPlain = kOffHalf + 2 * 128 * 4;         // [2][8]
+constexpr int kSmem = kOffPlain + 64 + 1024;
+static_assert(kSmem <= 232448, "shared memory");
+
+enum : int {
+    B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_COL = 30, B_HALF = 32,
+    B_DRAIN = 34, B_COUNT = 35
+};
+
+constexpr int kMaxClusters = cache_attn::kMaxClusters;
+constexpr int kTileCost = 1;     // of a tile's keys and epilogue, in steps
+constexpr int kMinWork = 6;      // least steps of a cluster
+
+// What the plan kernel writes: rows and keys of a sequence, and where its
+// tiles start on the line of work.
+struct SeqPlan {
+    int t_min, t_max;       // its rows lie in [t_min, t_max]
+    int hi, lo;             // keys that they see lie in [lo, hi] and [0, sink_end)
+    long long start;
+    long long pad;
+};
+struct Header {
+    long long total;
+    int ncl, pad;
+    int first[kMaxClusters];      // sequence in which a cluster's piece starts
+};
+// A tile whose partial sums cluster c_last's descriptor names.
+struct SplitTile {
+    int b, tile;                 // b < 0: none
+    int c_first, c_last;
+    long long base;
+    long long pad;
+};
+
+constexpr size_t kHeaderBytes = 512;
+constexpr size_t kDescBytes = kMaxClusters * sizeof(SplitTile);
+constexpr size_t kPartBytes = (size_t)kMaxClusters * 2 * kTile * 4;
+static_assert(sizeof(Header) <= kHeaderBytes, "header");
+constexpr size_t kFixedBytes = (kHeaderBytes + kDescBytes + kPartBytes + 255) / 256 * 256;
+
+__host__ __device__ __forceinline__ size_t ws_bytes(int n_seqs) { return kFixedBytes + (size_t)n_seqs * sizeof(SeqPlan); }
+
+struct Ws {
+    Header* head;
+    SplitTile* desc;
+    float* parts;
+    SeqPlan* seqs;
+};
+
+__host__ __device__ __forceinline__ Ws ws_of(void* p)
+{
+    uint8_t* b = reinterpret_cast<uint8_t*>(p);
+    Ws w;
+    w.head = reinterpret_cast<Header*>(b);
+    w.desc = reinterpret_cast<SplitTile*>(b + kHeaderBytes);
+    w.parts = reinterpret_cast<float*>(b + kHeaderBytes + kDescBytes);
+    w.seqs = reinterpret_cast<SeqPlan*>(b + kFixedBytes);
+    return w;
+}
+
+// Tiles of a sequence: those of the first tokens, then from lo on.
+struct Tiles {
+    int ns, m0, nt;
+    __device__ __forceinline__ int key0(int i) const { return (i < ns ? i : m0 + i - ns) * kTile; }
+};
+
+__device__ __forceinline__ Tiles tiles_of(int lo, int hi, int sink_end)
+{
+    Tiles r;
+    r.ns = r.m0 = r.nt = 0;
+    if (hi < 0) return r;
+    r.ns = (min(sink_end, hi + 1) + kTile - 1) / kTile;
+    r.m0 = max(r.ns, lo / kTile);
+    r.nt = r.ns + max(0, hi / kTile - r.m0 + 1);
+    return r;
+}
+
+__device__ __forceinline__ int rows_per_step(int Hq) { return kPairs / Hq; }
+__device__ __forceinline__ int steps_of(const SeqPlan& s, int Hq)
+{
+    return s.t_max < s.t_min ? 0 : (s.t_max - s.t_min) / rows_per_step(Hq) + 1;
+}
+__device__ __forceinline__ long long piece_begin(long long total, int ncl, int c) { return total * c / ncl; }
+
+constexpr int kPlanThreads = 1024;
+
+// One CTA: rows and keys of each sequence, then the line of work.
+__global__ void __launch_bounds__(kPlanThreads)
+cache_mass_plan_kernel(const Args a, int clusters, void* ws)
+{
+    __shared__ long long wsum[32];
+    const Ws w = ws_of(ws);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_wait();
+    for (int b = tid; b < a.pg.n_seqs; b += kPlanThreads) {
+        SeqPlan s;
+        s.t_min = INT_MAX;
+        s.t_max = -1;
+        s.hi = -1;
+        s.lo = INT_MAX;
+        s.start = s.pad = 0;
+        w.seqs[b] = s;
+    }
+    for (int c = tid; c < clusters; c += kPlanThreads) w.desc[c].b = -1;
+    __syncthreads();
+    const int sink_end = a.window > 0 ? a.sinks : 0;
+    for (int t0 = 0; t0 < a.T; t0 += kPlanThreads) {
+        const int t = t0 + tid;
+        int b = -1, hi = -1, lo = INT_MAX;
+        if (t < a.T) {
+            long long base;
+            const int* bt;
+            const int n = row_keys(a.pg, a.pos, nullptr, t, a.T, 0, &base, &bt);
+            if (n > 0) {
+                const Visible v = visible_of(n, a.pos[t], a.window, a.sinks);
+                b = a.pg.seq[t];
+                hi = v.hi;
+                lo = v.lo;
+            }
+        }
+        int same = 0;
+        __match_all_sync(0xffffffffu, b, &same);
+        int t_min = t, t_max = t;
+        bool mine = b >= 0;
+        if (same) {
+            t_min = __reduce_min_sync(0xffffffffu, t);
+            t_max = __reduce_max_sync(0xffffffffu, t);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            mine = mine && lane == 0;
+        }
+        if (mine) {
+            atomicMin(&w.seqs[b].t_min, t_min);
+            atomicMax(&w.seqs[b].t_max, t_max);
+            atomicMax(&w.seqs[b].hi, hi);
+            atomicMin(&w.seqs[b].lo, lo);
+        }
+    }
+    __syncthreads();
+    const int per = ceil_div(a.pg.n_seqs, kPlanThreads);
+    const int b0 = min(a.pg.n_seqs, tid * per), b1 = min(a.pg.n_seqs, b0 + per);
+    auto cost = [&](int b) -> long long {
+        SeqPlan s;
+        s.t_min = __ldcg(&w.seqs[b].t_min);
+        s.t_max = __ldcg(&w.seqs[b].t_max);
+        const Tiles k = tiles_of(__ldcg(&w.seqs[b].lo), __ldcg(&w.seqs[b].hi), sink_end);
+        return (long long)k.nt * (steps_of(s, a.Hq) + kTileCost);
+    };
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += cost(b);
+    long long pre = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
+    }
+    if (lane == 31) wsum[warp] = pre;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int i = 0; i < 32; ++i) {
+        if (i < warp) base += wsum[i];
+        total += wsum[i];
+    }
+    pre += base - sum;
+    const int ncl = total == 0 ? 0 : (int)max(1ll, min((long long)clusters, total / kMinWork));
+    if (tid == 0) {
+        w.head->total = total;
+        w.head->ncl = ncl;
+    }
+    for (int b = b0; b < b1; ++b) {
+        w.seqs[b].start = pre;
+        const long long c_b = cost(b);
+        if (c_b > 0)
+            for (int c = (int)((pre * ncl + total - 1) / total); c < ncl && piece_begin(total, ncl, c) < pre + c_b; ++c)
+                w.head->first[c] = b;
+        pre += c_b;
+    }
+}
+
+// Rows [t0, t0 + n) as a step of sequence b (a whole warp takes part): what
+// those of them that belong to b see.
+struct StepRange {
+    int hi, min_hi, lo, max_lo;
+    bool all;            // every one belongs to b and sees a key
+};
+
+__device__ __forceinline__ StepRange step_range(const Args& a, int b, int t0, int n)
+{
+    StepRange r;
+    r.hi = -1;
+    r.min_hi = r.lo = INT_MAX;
+    r.max_lo = 0;
+    bool all = true;
+    for (int i = threadIdx.x & 31; i < n; i += 32) {
+        const int t = t0 + i;
+        long long base;
+        const int* bt;
+        const int k = a.pg.seq[t] == b ? row_keys(a.pg, a.pos, nullptr, t, a.T, 0, &base, &bt) : 0;
+        if (k > 0) {
+            const Visible v = visible_of(k, a.pos[t], a.window, a.sinks);
+            r.hi = max(r.hi, v.hi);
+            r.min_hi = min(r.min_hi, v.hi);
+            r.lo = min(r.lo, v.lo);
+            r.max_lo = max(r.max_lo, v.lo);
+        } else {
+            all = false;
+        }
+    }
+    r.hi = __reduce_max_sync(0xffffffffu, r.hi);
+    r.min_hi = __reduce_min_sync(0xffffffffu, r.min_hi);
+    r.lo = __reduce_min_sync(0xffffffffu, r.lo);
+    r.max_lo = __reduce_max_sync(0xffffffffu, r.max_lo);
+    r.all = __all_sync(0xffffffffu, all);
+    return r;
+}
+
+// One step of a cluster's piece.
+struct Step {
+    int b, tile, key0, hi_b;   // sequence, its tile, the tile's first key, the last key any of its rows sees
+    int t0, n;                 // rows; n = 0: no row of this share sees the tile (partial sums of zero are due)
+    StepRange rg;
+    bool split;
+    long long base;            // the tile's place on the line of work
+};
+
+struct StepWalk {
+    long long w0, w1, total, base;
+    int ncl, b, tile, q, q1, nq;
+    bool in_tile, any;
+    SeqPlan s;
+    Tiles k;
+    __device__ __forceinline__ void load(const Args& a, const Ws& w)
+    {
+        while (b < a.pg.n_seqs) {
+            s = w.seqs[b];
+            k = tiles_of(s.lo, s.hi, a.window > 0 ? a.sinks : 0);
+            nq = steps_of(s, a.Hq);
+            if (k.nt > 0) return;
+            ++b;
+        }
+    }
+    __device__ __forceinline__ StepWalk(const Args& a, const Ws& w, int cid)
+    {
+        total = w.head->total;
+        ncl = w.head->ncl;
+        in_tile = any = false;
+        b = a.pg.n_seqs;
+        w0 = w1 = base = 0;
+        tile = q = q1 = nq = 0;
+        if (cid >= ncl) return;
+        w0 = piece_begin(total, ncl, cid);
+        w1 = piece_begin(total, ncl, cid + 1);
+        b = w.head->first[cid];
+        load(a, w);
+        tile = (int)((w0 - s.start) / (nq + kTileCost));
+        base = s.start + (long long)tile * (nq + kTileCost);
+    }
+    __device__ __forceinline__ bool next(const Args& a, const Ws& w, Step& st)
+    {
+        while (b < a.pg.n_seqs && base < w1) {
+            const long long d = base + kTileCost;
+            if (!in_tile) {
+                q = (int)max(0ll, min((long long)nq, w0 - d));
+                q1 = (int)max(0ll, min((long long)nq, w1 - d));
+                in_tile = true;
+                any = false;
+                st.split = q < q1 && (q > 0 || q1 < nq);
+            } else {
+                const int qa = (int)max(0ll, min((long long)nq, w0 - d));
+                st.split = qa > 0 || q1 < nq;
+            }
+            st.b = b;
+            st.tile = tile;
+            st.key0 = k.key0(tile);
+            st.hi_b = s.hi;
+            st.base = base;
+            const int G = rows_per_step(a.Hq), sink_end = a.window > 0 ? a.sinks : 0;
+            while (q < q1) {
+                st.t0 = s.t_min + q * G;
+                st.n = min(G, s.t_max + 1 - st.t0);
+                st.rg = step_range(a, b, st.t0, st.n);
+                ++q;
+                if (st.key0 <= st.rg.hi && (st.key0 + kTile > st.rg.lo || st.key0 < sink_end)) {
+                    any = true;
+                    return true;
+                }
+            }
+            // the tile's share is over
+            in_tile = false;
+            const bool due = st.split && !any;
+            base += nq + kTileCost;
+            if (++tile == k.nt) {
+                ++b;
+                tile = 0;
+                load(a, w);
+            }
+            if (due) {
+                st.n = 0;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q128,
+                     const __grid_constant__ CUtensorMap tm_q64, const float* __restrict__ lse, const Args args,
+                     float scale_log2, void* ws_raw, float* __restrict__ mass)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* sgen = smem_raw + (sbase - raw);
+    const uint32_t bar0 = sbase + kOffBar;
+    uint32_t* taddr_slot = reinterpret_cast<uint32_t*>(sgen + kOffBar + 8 * B_COUNT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + kOffBar + 8 * B_COUNT + 8);
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cid = (int)(blockIdx.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kSlabs; ++k) {
+            mbar_init(bar(B_KFULL + k), 1);
+            mbar_init(bar(B_KEMPTY + k), 1);
+        }
+        for (int s = 0; s < kQSlots; ++s) {
+            mbar_init(bar(B_QFULL + s), 1);
+            mbar_init(bar(B_QEMPTY + s), 1);
+        }
+        for (int d = 0; d < 2; ++d) {
+            mbar_init(bar(B_DFULL + d), 1);
+            mbar_init(bar(B_DFREE + d), 16);    // the summing warps of both CTAs
+            mbar_init(bar(B_COL + d), 8);
+            mbar_init(bar(B_HALF + d), 4);
+        }
+        mbar_init(bar(B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init_cluster();
+    }
+    if (warp == 9) {
+        tmem_alloc_pair(smem_u32(taddr_slot), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers exist before any remote arrival
+    tc_fence_after();
+    griddep_wait();
+    const uint32_t tmem = *taddr_slot;
+    const uint32_t el = elect_one();
+    const Ws ws = ws_of(ws_raw);
+    bool issued_any = false;
+    // pairs of a step as the MMA's N
+    auto n_of = [&](const Step& s) -> int { return s.n * args.Hq > 128 ? 256 : 128; };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ loads
+        if (el) {
+            prefetch_tmap(&tm_kv);
+            prefetch_tmap(&tm_q128);
+            prefetch_tmap(&tm_q64);
+        }
+        const uint32_t kfull0 = mapa(bar(B_KFULL), 0), qfull0 = mapa(bar(B_QFULL), 0);
+        int slot = 0, n_tiles = 0, last_b = -1, last_tile = -1;
+        uint32_t ph = 0;
+        bool ok = true;
+        StepWalk walk(args, ws, cid);
+        Step st;
+        while (ok && walk.next(args, ws, st)) {
+            if (st.n == 0) continue;
+            const bool fresh = st.b != last_b || st.tile != last_tile;
+            int row0 = 0, row1 = 0;
+            if (fresh) {
+                last_b = st.b;
+                last_tile = st.tile;
+                // blocks of 64 keys behind the last key seen read that key's
+                const int* bt = args.pg.block_table + (size_t)st.b * args.pg.max_pages;
+                const int s0 = st.key0 + 128 * (int)rank, top = st.hi_b / 64 * 64;
+                row0 = (int)key_row(args.pg, bt, 0, min(s0, top));
+                row1 = (int)key_row(args.pg, bt, 0, min(s0 + 64, top));
+            }
+            const int N = n_of(st);
+            const int qrow = st.t0 * args.Hq + (int)rank * (N / 2);
+            for (int k = 0; k < kSlabs; ++k) {
+                // a fresh tile waits for its slab of keys, too
+                const bool two = fresh && lane == 1;
+                ok = wait_lanes(two ? bar(B_KEMPTY + k) : bar(B_QEMPTY + slot), two ? (uint32_t)((n_tiles & 1) ^ 1) : ph ^ 1u,
+                                abort_flag, 2000 + k, n_tiles);
+                if (!ok) break;
+                if (el) {
+                    if (fresh) {
+                        if (rank == 0) mbar_arrive_expect_tx(bar(B_KFULL + k), 2 * kKSlab);
+                        const uint32_t dst = sbase + kOffK + k * kKSlab;
+                        tma_load_3d_pair(dst, &tm_kv, 0, row0, k, kfull0 + 8u * (uint32_t)k);
+                        tma_load_3d_pair(dst + kKSlab / 2, &tm_kv, 0, row1, k, kfull0 + 8u * (uint32_t)k);
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(bar(B_QFULL + slot), (uint32_t)N * 128u);
+                    tma_load_3d_pair(sbase + kOffQ + slot * kQSlot, N == 256 ? &tm_q128 : &tm_q64, 0, qrow, k,
+                                     qfull0 + 8u * (uint32_t)slot);
+                }
+                __syncwarp();
+                if (++slot == kQSlots) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (fresh) ++n_tiles;
+        }
+        if (!ok) {
+            // given up: copies in flight land before the CTA gives its shared memory up
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000ull) {
+            }
+        }
+    } else if (warp == 9 && rank == 0) {
+        // ---------------------------------------------------------- MMA issue
+        const uint64_t d_k = smem_desc(sbase + kOffK, 16, 1024, kSwizzle128B);
+        const uint64_t d_q = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+        int slot = 0, g = 0, n_tiles = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        StepWalk walk(args, ws, cid);
+        Step cur, nxt;
+        auto advance = [&](Step& s) -> bool {
+            while (walk.next(args, ws, s))
+                if (s.n > 0) return true;
+            return false;
+        };
+        bool have = advance(cur), fresh = true;
+        while (ok && have) {
+            const bool more = advance(nxt);
+            const bool last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
+            const uint32_t idesc = n_of(cur) == 256 ? idesc_bf16(256, 256, false) : idesc_bf16(256, 128, false);
+            const uint32_t d = tmem + (uint32_t)(g & 1) * 256;
+            for (int k = 0; k < kSlabs && ok; ++k) {
+                // lane 0: Q, lane 1: the keys of a fresh tile, lane 2: D read (step g - 2)
+                uint32_t wb = bar(B_QFULL + slot), wp = ph;
+                if (lane == 1 && fresh) {
+                    wb = bar(B_KFULL + k);
+                    wp = (uint32_t)(n_tiles & 1);
+                }
+                if (lane == 2 && k == 0 && g >= 2) {
+                    wb = bar(B_DFREE + (g & 1));
+                    wp = (uint32_t)(((g - 2) >> 1) & 1);
+                }
+                ok = wait_lanes(wb, wp, abort_flag, 2100 + k, g);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ak = d_k + (uint64_t)(k * (kKSlab >> 4)), bq = d_q + (uint64_t)(slot * (kQSlot >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_pair_ss(d, ak + kk * 2, bq + kk * 2, idesc, (k > 0 || kk > 0) ? 1u : 0u, el);
+                issued_any = true;
+                mma_commit_pair(bar(B_QEMPTY + slot), el);
+                if (last) mma_commit_pair(bar(B_KEMPTY + k), el);
+                if (++slot == kQSlots) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            mma_commit_pair(bar(B_DFULL + (g & 1)), el);
+            if (last) ++n_tiles;
+            fresh = last;
+            ++g;
+            cur = nxt;
+            have = more;
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------- sums
+        // TMEM lane i holds key i of this CTA's 128; hs takes half of the columns.
+        const int hs = warp >> 2, tid = (int)threadIdx.x;
+        const int i = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        float* col_f = reinterpret_cast<float*>(sgen + kOffCol);
+        float* half_s = reinterpret_cast<float*>(sgen + kOffHalf);
+        int* plain_s = reinterpret_cast<int*>(sgen + kOffPlain);
+        const uint32_t dfree0 = mapa(bar(B_DFREE), 0);
+        const int S = args.pg.max_pages * args.pg.page_size;
+        const int sink_end = args.window > 0 ? args.sinks : 0;
+        bool ok = true;
+        StepWalk walk(args, ws, cid);
+        Step cur, nxt;
+        // column tid of a step: its lse and the keys that its row sees
+        float c_lse = 0.f;
+        int c_hi = -1, c_lo = 0;
+        auto fetch = [&](const Step& s) {
+            c_hi = -1;
+            c_lo = 0;
+            c_lse = 0.f;
+            if (tid >= s.n * args.Hq) return;
+            const int t = s.t0 + tid / args.Hq;
+            if (args.pg.seq[t] != s.b) return;
+            long long base;
+            const int* bt;
+            const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
+            const float v = lse[(size_t)s.t0 * args.Hq + tid];
+            if (n <= 0 || v == -INFINITY) return;
+            const Visible vis = visible_of(n, args.pos[t], args.window, args.sinks);
+            c_hi = vis.hi;
+            c_lo = vis.lo;
+            c_lse = v * 1.4426950408889634f;
+        };
+        bool have = walk.next(args, ws, cur);
+        if (have && cur.n > 0) fetch(cur);
+        int g = 0, tiles = 0;
+        float sum = 0.f;
+        while (ok && have) {
+            const bool more = walk.next(args, ws, nxt);
+            const bool last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
+            const int key = cur.key0 + 128 * (int)rank + i;
+            if (cur.n > 0) {
+                const int buf = g & 1;
+                float* cl = col_f + buf * 3 * kPairs;
+                int* ch = reinterpret_cast<int*>(cl + kPairs);
+                int* co = ch + kPairs;
+                cl[tid] = c_lse;
+                ch[tid] = c_hi;
+                co[tid] = c_lo;
+                const bool used = __all_sync(0xffffffffu, c_hi >= 0);
+                if (lane == 0) plain_s[buf * 8 + warp] = used ? 1 : 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_COL + buf));
+                if (more && nxt.n > 0) fetch(nxt);
+                if (!wait_all(bar(B_COL + buf), (g >> 1) & 1, abort_flag, 2200, g)) { ok = false; break; }
+                const int N = n_of(cur);
+                const int k0 = cur.key0 + 128 * (int)rank;
+                bool whole = cur.rg.all && k0 + 127 <= cur.rg.min_hi && (k0 >= cur.rg.max_lo || k0 + 128 <= sink_end);
+                for (int w = 0; w < N / 32; ++w) whole = whole && plain_s[buf * 8 + w] != 0;
+                if (!wait_all(bar(B_DFULL + buf), (g >> 1) & 1, abort_flag, 2210, g)) { ok = false; break; }
+                tc_fence_after();
+                const int per = N / 2;
+                const uint32_t ta = tmem + lane_addr + (uint32_t)buf * 256 + hs * per;
+                float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll 1
+                for (int c0 = 0; c0 < per; c0 += 32) {
+                    uint32_t d[32];
+                    tmem_ld32(ta + c0, d);
+                    tmem_wait_ld();
+                    const float4* l4 = reinterpret_cast<const float4*>(cl + hs * per + c0);
+                    if (whole) {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const float4 l = l4[v];
+                            acc0 += ex2(fmaf(__uint_as_float(d[4 * v]), scale_log2, -l.x));
+                            acc1 += ex2(fmaf(__uint_as_float(d[4 * v + 1]), scale_log2, -l.y));
+                            acc0 += ex2(fmaf(__uint_as_float(d[4 * v + 2]), scale_log2, -l.z));
+                            acc1 += ex2(fmaf(__uint_as_float(d[4 * v + 3]), scale_log2, -l.w));
+                        }
+                    } else {
+                        const int4* h4 = reinterpret_cast<const int4*>(ch + hs * per + c0);
+                        const int4* o4 = reinterpret_cast<const int4*>(co + hs * per + c0);
+                        auto term = [&](uint32_t x, float l, int h, int o) -> float {
+                            const bool seen = key <= h && (key >= o || key < sink_end);
+                            return seen ? ex2(fmaf(__uint_as_float(x), scale_log2, -l)) : 0.f;
+                        };
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const float4 l = l4[v];
+                            const int4 h = h4[v], o = o4[v];
+                            acc0 += term(d[4 * v], l.x, h.x, o.x);
+                            acc1 += term(d[4 * v + 1], l.y, h.y, o.y);
+                            acc0 += term(d[4 * v + 2], l.z, h.z, o.z);
+                            acc1 += term(d[4 * v + 3], l.w, h.w, o.w);
+                        }
+                    }
+                }
+                sum += acc0 + acc1;
+                tc_fence_before();
+                __syncwarp();
+                // the loads' results are here, so the signal need not order them
+                if (lane == 0) mbar_arrive_remote_relaxed(dfree0 + 8u * (uint32_t)buf);
+                ++g;
+            } else if (more && nxt.n > 0) {
+                fetch(nxt);
+            }
+            if (last) {
+                // both column halves of a key, then its sum
+                float* hv = half_s + (tiles & 1) * 128;
+                if (hs == 1) {
+                    hv[i] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_HALF + (tiles & 1)));
+                } else {
+                    if (!wait_all(bar(B_HALF + (tiles & 1)), (tiles >> 1) & 1, abort_flag, 2220, g)) { ok = false; break; }
+                    const float total = sum + hv[i];
+                    if (cur.split) {
+                        const int place = cur.base < walk.w0 ? 0 : 1;
+                        ws.parts[((size_t)cid * 2 + place) * kTile + 128 * rank + i] = total;
+                    } else if (key < S && total != 0.f) {
+                        mass[(size_t)cur.b * S + key] += total;
+                    }
+                }
+                if (rank == 0 && threadIdx.x == 0 && cur.split) {
+                    // the cluster of the tile's last step names it for the join
+                    const SeqPlan sp = ws.seqs[cur.b];
+                    const long long end = cur.base + kTileCost + steps_of(sp, args.Hq);
+                    if (end <= walk.w1) {
+                        SplitTile d;
+                        d.b = cur.b;
+                        d.tile = cur.key0;
+                        d.c_first = (int)(((cur.base + kTileCost + 1) * walk.ncl - 1) / walk.total);
+                        d.c_last = cid;
+                        d.base = cur.base;
+                        d.pad = 0;
+                        ws.desc[cid] = d;
+                    }
+                }
+                sum = 0.f;
+                ++tiles;
+            }
+            cur = nxt;
+            have = more;
+        }
+    }
+
+    if (warp == 9 && issued_any) {
+        // every MMA issued completes before TMEM is released
+        mma_commit_pair(bar(B_DRAIN), el);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar(B_DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' MMAs, remote arrivals and copies are over
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc_pair(tmem, 512);
+    cluster_sync();
+}
+
+// Adds the partial sums of split tiles, in the order of the clusters.
+__global__ void __launch_bounds__(kTile)
+cache_mass_join_kernel(const void* ws_raw, int S, float* __restrict__ mass)
+{
+    griddep_wait();
+    const Ws w = ws_of(const_cast<void*>(ws_raw));
+    const SplitTile d = w.desc[blockIdx.x];
+    if (d.b < 0) return;
+    const long long total = w.head->total;
+    const int ncl = w.head->ncl;
+    float sum = 0.f;
+    for (int c = d.c_first; c <= d.c_last; ++c)
+        sum += w.parts[((size_t)c * 2 + (d.base < piece_begin(total, ncl, c) ? 0 : 1)) * kTile + threadIdx.x];
+    const int key = d.tile + (int)threadIdx.x;
+    if (key < S && sum != 0.f) mass[(size_t)d.b * S + key] += sum;
+}
+
+}  // namespace cache_mass
+}  // namespace dsa

@@ -21,6 +21,7 @@
 #include "attn_tc.cuh"
 #include "cache_attn.cuh"
 #include "cache_attn_tc.cuh"
+#include "cache_mass_tc.cuh"
 #include "cache_evict.cuh"
 #include "common.cuh"
 #include "debug_checks.cuh"
@@ -740,12 +741,13 @@ int make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t row
 }
 
 // A row-major bf16 [rows, 64 * slabs] matrix as [slabs][rows][64]: a box holds
-// box_slabs slabs of 64 columns x 64 rows, each in 128B-swizzled order.
-int make_tmap_slabs(CUtensorMap* m, const void* base, uint64_t slabs, uint64_t rows, uint32_t box_slabs)
+// box_slabs slabs of 64 columns x box_rows rows, each in 128B-swizzled order.
+int make_tmap_slabs(CUtensorMap* m, const void* base, uint64_t slabs, uint64_t rows, uint32_t box_slabs,
+                    uint32_t box_rows = 64)
 {
     const cuuint64_t dims[3] = {64, rows, slabs};
     const cuuint64_t strides[2] = {slabs * 128, 128};
-    const cuuint32_t box[3] = {64, 64, box_slabs};
+    const cuuint32_t box[3] = {64, box_rows, box_slabs};
     const cuuint32_t estr[3] = {1, 1, 1};
     EncodeTiledFn enc = encode_tiled();
     if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
@@ -1200,6 +1202,19 @@ dsa::PagedRows paged_rows(const int32_t* block_table, const int32_t* seq, int n_
     pg.num_pages = num_pages;
     return pg;
 }
+
+dsa::cache_attn::Args cache_attn_args(const dsa::PagedRows& pg, const int32_t* pos, int T, int Hq, int window,
+                                      int sinks)
+{
+    dsa::cache_attn::Args a;
+    a.pg = pg;
+    a.pos = pos;
+    a.T = T;
+    a.Hq = Hq;
+    a.window = window;
+    a.sinks = sinks;
+    return a;
+}
 }  // namespace
 
 size_t dsa_mla_attn_paged_workspace_size(int T, int Hq)
@@ -1233,13 +1248,7 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     cudaError_t e = cudaFuncSetAttribute(mla_attn_paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kTcSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_attn_paged_tc_kernel)");
-    Args args;
-    args.pg = pg;
-    args.pos = pos;
-    args.T = T;
-    args.Hq = Hq;
-    args.window = window;
-    args.sinks = sinks;
+    const Args args = cache_attn_args(pg, pos, T, Hq, window, sinks);
     float* part_o = reinterpret_cast<float*>(workspace);
     float* part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kPartBytes);
     SplitDesc* desc = reinterpret_cast<SplitDesc*>(reinterpret_cast<char*>(workspace) + kPartBytes + kPartLseBytes);
@@ -1261,23 +1270,42 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     return DSA_OK;
 }
 
+size_t dsa_mla_attn_mass_paged_workspace_size(int n_seqs)
+{
+    return n_seqs <= 0 ? 0 : dsa::cache_mass::ws_bytes(n_seqs);
+}
+
 int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, int page_size,
                             const int32_t* block_table, int n_seqs, int max_pages, const int32_t* seq,
                             const int32_t* pos, const float* lse, int T, int Hq, int d_qk, float scale, int window,
-                            int sinks, float* mass, void* stream)
+                            int sinks, float* mass, void* workspace, size_t ws_bytes, void* stream)
 {
-    using namespace dsa::cache_attn;
+    using namespace dsa::cache_mass;
     g_err[0] = 0;
     if (int rc = check_cache_attn(q, kv_pages, num_pages, page_size, block_table, n_seqs, max_pages, seq, pos, lse,
                                   T, Hq, d_qk, window, sinks))
         return rc;
     if (!mass || !al16(mass)) return fail(DSA_ERR_ARG, "mass must be a 16-byte aligned pointer");
+    const size_t need = dsa_mla_attn_mass_paged_workspace_size(n_seqs);
+    if (!workspace || ws_bytes < need || !al16(workspace))
+        return fail(DSA_ERR_WORKSPACE, "received weights need %zu workspace bytes (got %zu)", need, ws_bytes);
     const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
-    const long long keys = (long long)n_seqs * max_pages * page_size;
-    mla_attn_mass_simple_kernel<<<(unsigned)((keys + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(kv_pages), pg, pos, lse, T,
-        Hq, scale, window, sinks, mass);
-    DSA_LAUNCH_CHECK("mla_attn_mass_simple_kernel");
+    CUtensorMap tk, tq128, tq64;
+    if (int rc = make_tmap_slabs(&tk, kv_pages, kSlabs, (uint64_t)num_pages * page_size, 1)) return rc;
+    if (int rc = make_tmap_slabs(&tq128, q, kSlabs, (uint64_t)T * Hq, 1, 128)) return rc;
+    if (int rc = make_tmap_slabs(&tq64, q, kSlabs, (uint64_t)T * Hq, 1)) return rc;
+    cudaError_t e = cudaFuncSetAttribute(cache_mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cache_mass_tc_kernel)");
+    const Args args = cache_attn_args(pg, pos, T, Hq, window, sinks);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int clusters = std::min(kMaxClusters, std::max(1, num_sms() / 2));
+    launch_pdl(cache_mass_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, args, clusters, workspace);
+    DSA_LAUNCH_CHECK("cache_mass_plan_kernel");
+    launch_pdl(cache_mass_tc_kernel, dim3(2 * clusters), dim3(kThreads), kSmem, st, tk, tq128, tq64, lse, args,
+               scale * 1.4426950408889634f, workspace, mass);
+    DSA_LAUNCH_CHECK("cache_mass_tc_kernel");
+    launch_pdl(cache_mass_join_kernel, dim3(clusters), dim3(kTile), 0, st, workspace, max_pages * page_size, mass);
+    DSA_LAUNCH_CHECK("cache_mass_join_kernel");
     return DSA_OK;
 }
 

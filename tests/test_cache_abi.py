@@ -41,13 +41,14 @@ def test_attention_refuses(lib, change, code):
     assert rc == code and lib.dsa_last_error() and dsa.launch_count() == before
 
 
-@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(mass=None), -1), (dict(mass=ODD), -1)])
+@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(mass=None), -1), (dict(mass=ODD), -1), (dict(max_pages=1 << 25), -2),
+                                                    (dict(ws=None), -5), (dict(ws=ODD), -5), (dict(ws_bytes=64), -5)])
 def test_weights_refuse(lib, change, code):
     a = {**ATTN, "mass": FAKE, **change}
     before = dsa.launch_count()
     rc = lib.dsa_mla_attn_mass_paged(a["q"], a["kv"], a["num_pages"], a["page_size"], a["bt"], a["n_seqs"],
                                      a["max_pages"], a["seq"], a["pos"], a["lse"], a["T"], a["Hq"], a["d_qk"], SC,
-                                     a["window"], a["sinks"], a["mass"], None)
+                                     a["window"], a["sinks"], a["mass"], a["ws"], ctypes.c_size_t(a["ws_bytes"]), None)
     assert rc == code and lib.dsa_last_error() and dsa.launch_count() == before
 
 
