@@ -184,6 +184,26 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// A launch in clusters of `size` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int size, cudaStream_t st,
+                           Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
 // ------------------------------------------------------------ workspace plan
 
 constexpr size_t kAlign = 256;
@@ -1324,8 +1344,14 @@ int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_le
         return fail(DSA_ERR_ARG, "sinks=%d and recent=%d must be >= 0 and at most keep=%d together", sinks, recent,
                     keep);
     if (max_len > kMaxLen) return fail(DSA_ERR_UNSUPPORTED, "max_len=%d (supported: up to %d)", max_len, kMaxLen);
-    cache_evict_select_kernel<<<n_seqs, kSelectThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        mass, max_len, seq_len, max_len, keep, sinks, recent, keep_idx, new_len);
+    // the smallest cluster whose registers hold a row of weights, at most 8 CTAs
+    int size = 1;
+    while (size < 8 && (long long)size * kSelRound < max_len) size *= 2;
+    if ((long long)n_seqs * size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
+    cudaError_t e = launch_cluster(cache_evict_select_kernel, dim3(n_seqs * size), dim3(kSelThreads), kSelSmem, size,
+                                   reinterpret_cast<cudaStream_t>(stream), mass, (long long)max_len, seq_len, max_len,
+                                   keep, sinks, recent, keep_idx, new_len);
+    if (e != cudaSuccess) return cuda_fail(e, "cache_evict_select_kernel");
     DSA_LAUNCH_CHECK("cache_evict_select_kernel");
     return DSA_OK;
 }
@@ -1351,20 +1377,27 @@ int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int
                     kv_row_bytes, k_row_bytes, kMaxRowBytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dsa::PagedRows pg = paged_rows(block_table, nullptr, n_seqs, max_pages, page_size, num_pages);
-    constexpr int slice = 128;
-    cache_compact_kernel<<<dim3(n_seqs, dsa::ceil_div(kv_row_bytes, slice)), kCompactThreads, 0, st>>>(
-        reinterpret_cast<uint8_t*>(kv_pages), kv_row_bytes, slice, pg, keep_idx, keep, new_len);
+    // Narrow slices and clusters of up to 8 CTAs where there are few sequences,
+    // so that the whole card takes part.
+    const int sms = num_sms();
+    const int slice = (long long)n_seqs * dsa::ceil_div(kv_row_bytes, 128) >= sms ? 128 : 64;
+    MoveRows kv, keys;
+    kv.rows = reinterpret_cast<uint8_t*>(kv_pages);
+    kv.bytes = kv_row_bytes;
+    kv.slices = dsa::ceil_div(kv_row_bytes, slice);
+    keys.rows = reinterpret_cast<uint8_t*>(k_pages);
+    keys.bytes = k_pages ? k_row_bytes : 0;
+    keys.slices = k_pages ? dsa::ceil_div(k_row_bytes, slice) : 0;
+    const int slices = kv.slices + keys.slices + (mass ? 1 : 0);
+    int size = 1;
+    while (size < 8 && (long long)n_seqs * slices * size < 2 * sms) size *= 2;
+    if ((long long)n_seqs * size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
+    cudaError_t e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cache_compact_kernel)");
+    e = launch_cluster(cache_compact_kernel, dim3(n_seqs * size, slices), dim3(kMoveThreads), kMoveSmem, size, st, kv,
+                       keys, mass, slice, pg, keep_idx, keep, new_len);
+    if (e != cudaSuccess) return cuda_fail(e, "cache_compact_kernel");
     DSA_LAUNCH_CHECK("cache_compact_kernel");
-    if (k_pages) {
-        cache_compact_kernel<<<dim3(n_seqs, dsa::ceil_div(k_row_bytes, slice)), kCompactThreads, 0, st>>>(
-            reinterpret_cast<uint8_t*>(k_pages), k_row_bytes, slice, pg, keep_idx, keep, new_len);
-        DSA_LAUNCH_CHECK("cache_compact_kernel");
-    }
-    if (mass) {
-        cache_compact_mass_kernel<<<n_seqs, kCompactThreads, 0, st>>>(mass, max_pages * page_size, keep_idx, keep,
-                                                                      new_len);
-        DSA_LAUNCH_CHECK("cache_compact_mass_kernel");
-    }
     return DSA_OK;
 }
 
