@@ -1344,11 +1344,17 @@ int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_le
         return fail(DSA_ERR_ARG, "sinks=%d and recent=%d must be >= 0 and at most keep=%d together", sinks, recent,
                     keep);
     if (max_len > kMaxLen) return fail(DSA_ERR_UNSUPPORTED, "max_len=%d (supported: up to %d)", max_len, kMaxLen);
-    // the smallest cluster whose registers hold a row of weights, at most 8 CTAs
+    // the smallest cluster whose shared memory holds a row of weights, more CTAs
+    // where there are few sequences, at most 8
     int size = 1;
-    while (size < 8 && (long long)size * kSelRound < max_len) size *= 2;
+    while (size < kSelMaxCluster && ((long long)size * kSelRound < max_len ||
+                                     ((long long)n_seqs * size < num_sms() && size * 4096 < max_len)))
+        size *= 2;
     if ((long long)n_seqs * size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
-    cudaError_t e = launch_cluster(cache_evict_select_kernel, dim3(n_seqs * size), dim3(kSelThreads), kSelSmem, size,
+    cudaError_t e = cudaFuncSetAttribute(cache_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSelSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cache_evict_select_kernel)");
+    e = launch_cluster(cache_evict_select_kernel, dim3(n_seqs * size), dim3(kSelThreads), kSelSmem, size,
                                    reinterpret_cast<cudaStream_t>(stream), mass, (long long)max_len, seq_len, max_len,
                                    keep, sinks, recent, keep_idx, new_len);
     if (e != cudaSuccess) return cuda_fail(e, "cache_evict_select_kernel");
