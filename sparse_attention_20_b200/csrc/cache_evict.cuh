@@ -56,11 +56,12 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums)
 // of the positions. The free places (keep - sinks - recent) go to the largest
 // weights of the unprotected positions [sinks, n - recent), ties to the lower
 // position: a radix select over the order key's bits, 11 + 11 + 10, finds the
-// last key that stays and how many of its equals do; each digit's histogram
-// is summed over the cluster's shared memory. Up to 16384 positions per CTA
-// the order keys stay in shared memory (three CTAs a SM; in registers only
-// one of 1024 threads fits, and 64 sequences took four rounds of the card: 151
-// us against 40); longer sequences read the weights again for each digit.
+// last key that stays and how many of its equals do. Each digit's histogram
+// is added up in the first CTA (only the bins in use cross the cluster), which
+// names the digit. Up to 16384 positions per CTA the order keys stay in shared
+// memory, three CTAs a SM; longer sequences read the weights again for each
+// pass. Work is bound by instructions, so positions are handled four a lane,
+// and protected ones are left out by an order key of 0, which no weight has.
 __global__ void __launch_bounds__(kSelThreads, 3)
 cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const int* __restrict__ seq_len,
                           int max_len, int keep, int sinks, int recent, int* __restrict__ keep_idx,
@@ -70,8 +71,8 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
     uint32_t* held = sel_smem;                                      // [kSelRound] order keys
     int* hist = reinterpret_cast<int*>(sel_smem + kSelRound);       // [kBins]
     __shared__ int wsum[kSelWarps];
-    __shared__ int s_digit, s_need;
-    __shared__ int counts[2];          // this CTA's positions above the cut (or protected), and equal to it
+    __shared__ int found[2];           // the digit and what is still needed of its bin (first CTA)
+    __shared__ int counts[2];          // this CTA's keys above the cut, and equal to it
     __shared__ int w_stay[kSelWarps], w_eq[kSelWarps];
     const int rank = (int)cluster_ctarank(), size = (int)cluster_size();
     const int b = (int)(blockIdx.x / size), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -84,99 +85,100 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
         return;
     }
     const int lo = sinks, hi = n - recent;   // unprotected
-    // this CTA's share [c0, c1) of the positions
+    for (int j = rank * kSelThreads + tid; j < sinks + recent; j += size * kSelThreads)
+        idx[j < sinks ? j : keep - recent + j - sinks] = j < sinks ? j : hi + j - sinks;
+    // this CTA's share [c0, c0 + 4 groups) of the positions
     const int share = (int)(((long long)n + (long long)size * 4 - 1) / ((long long)size * 4)) * 4;
-    const int c0 = min(n, rank * share), c1 = min(n, c0 + share);
+    const int c0 = min(n, rank * share), c1 = min(n, c0 + share), groups = (c1 - c0 + 3) / 4;
     const bool in_smem = share <= kSelRound;
+    const bool quads = (reinterpret_cast<uintptr_t>(row + c0) & 15u) == 0;
+    // order keys of positions c0 + 4 g .. + 3, 0 where protected
+    auto fetch = [&](int g) -> uint4 {
+        const int s = c0 + 4 * g;
+        if (quads && s >= lo && s + 4 <= hi) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(row + s));
+            return make_uint4(mass_key(v.x), mass_key(v.y), mass_key(v.z), mass_key(v.w));
+        }
+        auto one = [&](int p) -> uint32_t { return p >= lo && p < hi ? mass_key(row[p]) : 0u; };
+        return make_uint4(one(s), one(s + 1), one(s + 2), one(s + 3));
+    };
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     if (in_smem) {
-        if ((reinterpret_cast<uintptr_t>(row + c0) & 15u) == 0) {
-#pragma unroll 8
-            for (int s = c0 + 4 * tid; s < c1; s += 4 * kSelThreads) {
-                float4 v;
-                if (s + 4 <= c1) {
-                    v = __ldg(reinterpret_cast<const float4*>(row + s));
-                } else {
-                    v.x = row[s];
-                    v.y = s + 1 < c1 ? row[s + 1] : 0.f;
-                    v.z = s + 2 < c1 ? row[s + 2] : 0.f;
-                    v.w = 0.f;
-                }
-                *reinterpret_cast<uint4*>(held + (s - c0)) = make_uint4(mass_key(v.x), mass_key(v.y), mass_key(v.z),
-                                                                       mass_key(v.w));
-            }
-        } else {
-#pragma unroll 8
-            for (int s = c0 + tid; s < c1; s += kSelThreads) held[s - c0] = mass_key(row[s]);
-        }
+#pragma unroll 4
+        for (int g = tid; g < groups; g += kSelThreads) *reinterpret_cast<uint4*>(held + 4 * g) = fetch(g);
     }
-    __syncthreads();
-    auto key_at = [&](int s) -> uint32_t { return in_smem ? held[s - c0] : mass_key(row[s]); };
+    auto keys_at = [&](int g) -> uint4 { return in_smem ? *reinterpret_cast<const uint4*>(held + 4 * g) : fetch(g); };
+    cluster_sync();                          // every histogram is zero
     uint32_t prefix = 0, known = 0;          // digits found so far and their bits
     int need = keep - sinks - recent;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-        const int s1 = min(c1, hi);
-#pragma unroll 8
-        for (int s = max(c0, lo) + tid; s < s1; s += kSelThreads) {
-            const uint32_t k = key_at(s);
+        auto tally = [&](uint32_t k) {
             if ((k & known) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+        };
+#pragma unroll 2
+        for (int g = tid; g < groups; g += kSelThreads) {
+            const uint4 k = keys_at(g);
+            tally(k.x);
+            tally(k.y);
+            tally(k.z);
+            tally(k.w);
         }
-        cluster_sync();
-        // bins from the top down, four per thread (bin index 4 tid' + 3 .. 4 tid'), summed over the cluster
-        const int top = bins - 4 - 4 * tid;
-        int v[4] = {0, 0, 0, 0};
-        if (top >= 0) {
-            uint4 part[kSelMaxCluster];
-#pragma unroll
-            for (int c = 0; c < kSelMaxCluster; ++c)
-                if (c < size) part[c] = sm100::ld_cluster_v4(mapa(smem_u32(hist + top), (uint32_t)c));
-#pragma unroll
-            for (int c = 0; c < kSelMaxCluster; ++c)
-                if (c < size) {
-                    v[0] += (int)part[c].w;
-                    v[1] += (int)part[c].z;
-                    v[2] += (int)part[c].y;
-                    v[3] += (int)part[c].x;
+        __syncthreads();
+        if (rank != 0) {
+            const uint32_t h0 = mapa(smem_u32(hist), 0);
+            for (int i = tid; i < bins; i += kSelThreads) {
+                const int v = hist[i];
+                if (v) {
+                    sm100::red_cluster_add(h0 + 4u * (uint32_t)i, (uint32_t)v);
+                    hist[i] = 0;
                 }
-        }
-        int before = block_scan(v[0] + v[1] + v[2] + v[3], wsum);
-        if (top >= 0 && before < need) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (before < need && before + v[e] >= need) {
-                    s_digit = top + 3 - e;
-                    s_need = need - before;
-                }
-                before += v[e];
             }
         }
-        // no free place: everything unprotected goes
-        if (tid == 0 && need == 0) {
-            s_digit = bins - 1;
-            s_need = 0;
+        cluster_sync();
+        if (rank == 0) {
+            // bins from the top down, four per thread
+            const int top = bins - 4 - 4 * tid;
+            int4 v = make_int4(0, 0, 0, 0);
+            if (top >= 0) {
+                v = *reinterpret_cast<const int4*>(hist + top);
+                *reinterpret_cast<int4*>(hist + top) = make_int4(0, 0, 0, 0);
+            }
+            int before = block_scan(v.x + v.y + v.z + v.w, wsum);
+            const int of[4] = {v.w, v.z, v.y, v.x};
+            if (top >= 0 && before < need) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (before < need && before + of[e] >= need) {
+                        found[0] = top + 3 - e;
+                        found[1] = need - before;
+                    }
+                    before += of[e];
+                }
+            }
+            // no free place: everything unprotected goes
+            if (tid == 0 && need == 0) {
+                found[0] = bins - 1;
+                found[1] = 0;
+            }
         }
-        cluster_sync();                // the histograms are read everywhere
-        prefix |= (uint32_t)s_digit << shift;
+        cluster_sync();
+        const uint32_t f0 = mapa(smem_u32(found), 0);
+        prefix |= sm100::ld_cluster_u32(f0) << shift;
+        need = (int)sm100::ld_cluster_u32(f0 + 4);
         known |= (uint32_t)(bins - 1) << shift;
-        need = s_need;
-        if (pass < 2)
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
     }
     // keys above `prefix` stay, and the first `need` of its equals; a warp's
-    // share is contiguous, 32 positions a step
-    const int wshare = (share / kSelWarps + 32) / 32 * 32;
-    const int w0 = min(c1, c0 + warp * wshare), w1 = min(c1, w0 + wshare);
-    auto stays = [&](int s, uint32_t k) -> bool { return s < lo || s >= hi || k > prefix; };
-    auto equals = [&](int s, uint32_t k) -> bool { return s >= lo && s < hi && k == prefix; };
+    // share is contiguous, 32 groups a step
+    const int wshare = (groups / kSelWarps + 32) / 32 * 32;
+    const int g0 = min(groups, warp * wshare), g1 = min(groups, g0 + wshare);
     int n_stay = 0, n_eq = 0;
 #pragma unroll 4
-    for (int s = w0 + lane; s < w1; s += 32) {
-        const uint32_t k = key_at(s);
-        n_stay += stays(s, k) ? 1 : 0;
-        n_eq += equals(s, k) ? 1 : 0;
+    for (int g = g0 + lane; g < g1; g += 32) {
+        const uint4 k = keys_at(g);
+        n_stay += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+        n_eq += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
     }
     n_stay = __reduce_add_sync(0xffffffffu, n_stay);
     n_eq = __reduce_add_sync(0xffffffffu, n_eq);
@@ -185,7 +187,7 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
         w_eq[warp] = n_eq;
     }
     __syncthreads();
-    int at = 0, eq_at = 0;             // stays and equals before this warp's share
+    int at = 0, eq_at = 0;             // keys above the cut and equals before this warp's share
     {
         int all_stay = 0, all_eq = 0;
         for (int w = 0; w < kSelWarps; ++w) {
@@ -206,19 +208,48 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
         at += (int)sm100::ld_cluster_u32(mapa(smem_u32(counts), (uint32_t)c));
         eq_at += (int)sm100::ld_cluster_u32(mapa(smem_u32(counts + 1), (uint32_t)c));
     }
-    cluster_sync();                    // no CTA leaves while another reads its counts
-    at += min(eq_at, need);
+    cluster_sync();                    // no CTA leaves while another reads its counts or its digit
+    at += lo + min(eq_at, need);
     const unsigned lower = (1u << lane) - 1u;
-    for (int s0 = w0; s0 < w1; s0 += 32) {
-        const int s = s0 + lane;
-        const uint32_t k = s < w1 ? key_at(s) : 0u;
-        const bool eq = s < w1 && equals(s, k);
-        const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-        const bool take = s < w1 && (stays(s, k) || (eq && eq_at + __popc(eqs & lower) < need));
-        const unsigned takes = __ballot_sync(0xffffffffu, take);
-        if (take) idx[at + __popc(takes & lower)] = s;
-        at += __popc(takes);
-        eq_at += __popc(eqs);
+    for (int gg = g0; gg < g1; gg += 32) {
+        const int g = gg + lane, s = c0 + 4 * g;
+        const uint4 kq = g < g1 ? keys_at(g) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[4] = {kq.x, kq.y, kq.z, kq.w};
+        unsigned take = 0;             // of this lane's four
+#pragma unroll
+        for (int e = 0; e < 4; ++e) take |= (k[e] > prefix ? 1u : 0u) << e;
+        if (eq_at < need) {            // equals still find a place (the same for the whole warp)
+            unsigned eq = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) eq |= (g < g1 && k[e] == prefix ? 1u : 0u) << e;
+            if (__any_sync(0xffffffffu, eq != 0)) {
+                int before = 0, all = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned m = __ballot_sync(0xffffffffu, (eq >> e) & 1u);
+                    before += __popc(m & lower);
+                    all += __popc(m);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((eq >> e) & 1u) {
+                        if (eq_at + before < need) take |= 1u << e;
+                        ++before;
+                    }
+                eq_at += all;
+            }
+        }
+        int place = at, all = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned m = __ballot_sync(0xffffffffu, (take >> e) & 1u);
+            place += __popc(m & lower);
+            all += __popc(m);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((take >> e) & 1u) idx[place++] = s + e;
+        at += all;
     }
 }
 

@@ -224,14 +224,9 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr)
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr)
+__device__ __forceinline__ void red_cluster_add(uint32_t cluster_addr, uint32_t v)
 {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(cluster_addr)
-                 : "memory");
-    return v;
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_v2(uint32_t cluster_addr, uint2 v)
 {
