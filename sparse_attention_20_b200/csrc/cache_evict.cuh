@@ -27,12 +27,13 @@ __device__ __forceinline__ uint32_t cluster_size()
 // Order key of a weight: larger is kept first; a NaN ranks with -inf.
 __device__ __forceinline__ uint32_t mass_key(float v) { return score_key(v == v ? v : -INFINITY); }
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 384;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelRound = 16384;                     // positions a CTA holds in shared memory
+constexpr int kSelHold = 11776;                      // positions a CTA holds in shared memory
+constexpr int kSelShare = 16384;                     // positions of a CTA where the cluster can grow
 constexpr int kBins = 2048;
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelSmem = kSelRound * 4 + kBins * 4;
+constexpr int kSelSmem = kSelHold * 4 + kBins * 4;
 
 // Block-wide exclusive sum of one int per thread.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums)
@@ -58,18 +59,20 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums)
 // position: a radix select over the order key's bits, 11 + 11 + 10, finds the
 // last key that stays and how many of its equals do. Each digit's histogram
 // is added up in the first CTA (only the bins in use cross the cluster), which
-// names the digit. Up to 16384 positions per CTA the order keys stay in shared
-// memory, three CTAs a SM; longer sequences read the weights again for each
+// names the digit. A CTA keeps the order keys of its first 11776 positions in
+// shared memory, so that four CTAs share a SM and 64 sequences of any length
+// run at once (with 16384 it is three, and the second round of the card took
+// as long as the first: 46 us against MEASURED); the others are read again for each
 // pass. Work is bound by instructions, so positions are handled four a lane,
 // and protected ones are left out by an order key of 0, which no weight has.
-__global__ void __launch_bounds__(kSelThreads, 3)
+__global__ void __launch_bounds__(kSelThreads, 4)
 cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const int* __restrict__ seq_len,
                           int max_len, int keep, int sinks, int recent, int* __restrict__ keep_idx,
                           int* __restrict__ new_len)
 {
     extern __shared__ __align__(16) uint32_t sel_smem[];
-    uint32_t* held = sel_smem;                                      // [kSelRound] order keys
-    int* hist = reinterpret_cast<int*>(sel_smem + kSelRound);       // [kBins]
+    uint32_t* held = sel_smem;                                      // [kSelHold] order keys
+    int* hist = reinterpret_cast<int*>(sel_smem + kSelHold);       // [kBins]
     __shared__ int wsum[kSelWarps];
     __shared__ int found[2];           // the digit and what is still needed of its bin (first CTA)
     __shared__ int counts[2];          // this CTA's keys above the cut, and equal to it
@@ -90,7 +93,7 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
     // this CTA's share [c0, c0 + 4 groups) of the positions
     const int share = (int)(((long long)n + (long long)size * 4 - 1) / ((long long)size * 4)) * 4;
     const int c0 = min(n, rank * share), c1 = min(n, c0 + share), groups = (c1 - c0 + 3) / 4;
-    const bool in_smem = share <= kSelRound;
+    const int n_held = min(groups, kSelHold / 4);
     const bool quads = (reinterpret_cast<uintptr_t>(row + c0) & 15u) == 0;
     // order keys of positions c0 + 4 g .. + 3, 0 where protected
     auto fetch = [&](int g) -> uint4 {
@@ -103,11 +106,9 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
         return make_uint4(one(s), one(s + 1), one(s + 2), one(s + 3));
     };
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    if (in_smem) {
 #pragma unroll 4
-        for (int g = tid; g < groups; g += kSelThreads) *reinterpret_cast<uint4*>(held + 4 * g) = fetch(g);
-    }
-    auto keys_at = [&](int g) -> uint4 { return in_smem ? *reinterpret_cast<const uint4*>(held + 4 * g) : fetch(g); };
+    for (int g = tid; g < n_held; g += kSelThreads) *reinterpret_cast<uint4*>(held + 4 * g) = fetch(g);
+    auto keys_at = [&](int g) -> uint4 { return g < n_held ? *reinterpret_cast<const uint4*>(held + 4 * g) : fetch(g); };
     cluster_sync();                          // every histogram is zero
     uint32_t prefix = 0, known = 0;          // digits found so far and their bits
     int need = keep - sinks - recent;
@@ -138,20 +139,25 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
         }
         cluster_sync();
         if (rank == 0) {
-            // bins from the top down, four per thread
-            const int top = bins - 4 - 4 * tid;
-            int4 v = make_int4(0, 0, 0, 0);
+            // bins from the top down, eight per thread
+            const int top = bins - 8 - 8 * tid;
+            int of[8] = {};
             if (top >= 0) {
-                v = *reinterpret_cast<const int4*>(hist + top);
-                *reinterpret_cast<int4*>(hist + top) = make_int4(0, 0, 0, 0);
-            }
-            int before = block_scan(v.x + v.y + v.z + v.w, wsum);
-            const int of[4] = {v.w, v.z, v.y, v.x};
-            if (top >= 0 && before < need) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
+                    of[e] = hist[top + 7 - e];
+                    hist[top + 7 - e] = 0;
+                }
+            }
+            int sum = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += of[e];
+            int before = block_scan(sum, wsum);
+            if (top >= 0 && before < need && before + sum >= need) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
                     if (before < need && before + of[e] >= need) {
-                        found[0] = top + 3 - e;
+                        found[0] = top + 7 - e;
                         found[1] = need - before;
                     }
                     before += of[e];

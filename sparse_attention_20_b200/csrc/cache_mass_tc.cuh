@@ -17,8 +17,10 @@
 // second kernel adds in order, so results do not depend on timing. Steps none
 // of whose rows sees a key of the tile are passed over.
 //
-// Warps (10 per CTA): 0-7 sums (two per TMEM lane quarter, half of the columns
-// each), 8 loads, 9 MMA issue (even CTA).
+// Warps (11 per CTA): 0-7 sums (two per TMEM lane quarter, half of the columns
+// each), 8 loads, 9 MMA issue (even CTA), 10 the next step's columns (lse, keys
+// seen), a step ahead of the sums: with the sums' own loads in their loop a
+// step took 8500 clocks instead of MEASURED.
 #pragma once
 #include <cuda.h>
 
@@ -39,7 +41,7 @@ constexpr int kDqk = cache_attn::kDqk;
 constexpr int kSlabs = kDqk / 64;
 constexpr int kTile = 256;                 // keys of a tile (both CTAs)
 constexpr int kPairs = 256;                // (row, head) pairs of a step
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kKSlab = 128 * 128;          // 128 keys x 64 columns
 constexpr int kQSlot = 128 * 128;          // 128 pairs x 64 columns
 constexpr int kQSlots = 4;
@@ -48,13 +50,13 @@ constexpr int kOffQ = kOffK + kSlabs * kKSlab;
 constexpr int kOffBar = kOffQ + kQSlots * kQSlot;
 constexpr int kOffCol = kOffBar + 512;                    // [2][256] lse2, last and first key seen
 constexpr int kOffHalf = kOffCol + 2 * 3 * kPairs * 4;    // [2][128] sums of the second column half
-constexpr int kOffPlain = kOffHalf + 2 * 128 * 4;         // [2][8]
-constexpr int kSmem = kOffPlain + 64 + 1024;
+constexpr int kOffStep = kOffHalf + 2 * 128 * 4;          // [2] StepInfo
+constexpr int kSmem = kOffStep + 2 * 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 
 enum : int {
-    B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_COL = 30, B_HALF = 32,
-    B_DRAIN = 34, B_COUNT = 35
+    B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_COL = 30, B_COLFREE = 32,
+    B_HALF = 34, B_DRAIN = 36, B_COUNT = 37
 };
 
 constexpr int kMaxClusters = cache_attn::kMaxClusters;
@@ -218,11 +220,22 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
     }
     for (int b = b0; b < b1; ++b) {
         w.seqs[b].start = pre;
-        const long long c_b = cost(b);
-        if (c_b > 0)
-            for (int c = (int)((pre * ncl + total - 1) / total); c < ncl && piece_begin(total, ncl, c) < pre + c_b; ++c)
-                w.head->first[c] = b;
-        pre += c_b;
+        pre += cost(b);
+    }
+    __syncthreads();
+    // the sequence in which each cluster's piece starts: the last one that starts
+    // no later (those without work start where the next one does)
+    if (tid < ncl) {
+        const long long w0 = piece_begin(total, ncl, tid);
+        int l = 0, r = a.pg.n_seqs - 1;
+        while (l < r) {
+            const int m = (l + r + 1) / 2;
+            if (__ldcg(&w.seqs[m].start) <= w0)
+                l = m;
+            else
+                r = m - 1;
+        }
+        w.head->first[tid] = l;
     }
 }
 
@@ -271,6 +284,17 @@ struct Step {
     bool split;
     long long base;            // the tile's place on the line of work
 };
+
+// What the summing warps need to know of a step.
+struct StepInfo {
+    int N;          // columns; 0: no step, only a share's end; -1: no more
+    int whole;      // every column sees each of this CTA's 128 keys
+    int last;       // the last step of this cluster's share of the tile
+    int b, key0;
+    int part;       // where its partial sums go, -1: the share is the whole tile
+    int pad[10];
+};
+static_assert(sizeof(StepInfo) == 64, "StepInfo");
 
 struct StepWalk {
     long long w0, w1, total, base;
@@ -381,7 +405,8 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         for (int d = 0; d < 2; ++d) {
             mbar_init(bar(B_DFULL + d), 1);
             mbar_init(bar(B_DFREE + d), 16);    // the summing warps of both CTAs
-            mbar_init(bar(B_COL + d), 8);
+            mbar_init(bar(B_COL + d), 1);
+            mbar_init(bar(B_COLFREE + d), 8);
             mbar_init(bar(B_HALF + d), 4);
         }
         mbar_init(bar(B_DRAIN), 1);
@@ -517,70 +542,128 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             cur = nxt;
             have = more;
         }
-    } else if (warp < 8) {
-        // ------------------------------------------------------------- sums
-        // TMEM lane i holds key i of this CTA's 128; hs takes half of the columns.
-        const int hs = warp >> 2, tid = (int)threadIdx.x;
-        const int i = (warp & 3) * 32 + lane;
-        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    } else if (warp == 10) {
+        // ------------------------------------------- columns of the steps
         float* col_f = reinterpret_cast<float*>(sgen + kOffCol);
-        float* half_s = reinterpret_cast<float*>(sgen + kOffHalf);
-        int* plain_s = reinterpret_cast<int*>(sgen + kOffPlain);
-        const uint32_t dfree0 = mapa(bar(B_DFREE), 0);
-        const int S = args.pg.max_pages * args.pg.page_size;
+        StepInfo* info = reinterpret_cast<StepInfo*>(sgen + kOffStep);
         const int sink_end = args.window > 0 ? args.sinks : 0;
+        int gd = 0;
         bool ok = true;
         StepWalk walk(args, ws, cid);
         Step cur, nxt;
-        // column tid of a step: its lse and the keys that its row sees
-        float c_lse = 0.f;
-        int c_hi = -1, c_lo = 0;
-        auto fetch = [&](const Step& s) {
-            c_hi = -1;
-            c_lo = 0;
-            c_lse = 0.f;
-            if (tid >= s.n * args.Hq) return;
-            const int t = s.t0 + tid / args.Hq;
-            if (args.pg.seq[t] != s.b) return;
-            long long base;
-            const int* bt;
-            const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
-            const float v = lse[(size_t)s.t0 * args.Hq + tid];
-            if (n <= 0 || v == -INFINITY) return;
-            const Visible vis = visible_of(n, args.pos[t], args.window, args.sinks);
-            c_hi = vis.hi;
-            c_lo = vis.lo;
-            c_lse = v * 1.4426950408889634f;
-        };
         bool have = walk.next(args, ws, cur);
-        if (have && cur.n > 0) fetch(cur);
+        while (ok) {
+            const int buf = gd & 1;
+            ok = wait_lanes(bar(B_COLFREE + buf), (uint32_t)(((gd >> 1) & 1) ^ 1), abort_flag, 2300, gd);
+            if (!ok) break;
+            if (!have) {
+                if (el) {
+                    info[buf].N = -1;
+                    mbar_arrive(bar(B_COL + buf));
+                }
+                break;
+            }
+            float* cl = col_f + buf * 3 * kPairs;
+            int* ch = reinterpret_cast<int*>(cl + kPairs);
+            int* co = ch + kPairs;
+            const int N = cur.n > 0 ? n_of(cur) : 0;
+            // a column's lse and the keys that its row sees (none: a column without a
+            // row of this sequence, or with nothing to give)
+            float v[8];
+            int hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = e * 32 + lane;
+                hi[e] = -1;
+                lo[e] = 0;
+                v[e] = -INFINITY;
+                if (c < cur.n * args.Hq) {
+                    const int t = cur.t0 + c / args.Hq;
+                    v[e] = __ldg(lse + (size_t)cur.t0 * args.Hq + c);
+                    if (args.pg.seq[t] == cur.b) {
+                        long long base;
+                        const int* bt;
+                        const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
+                        if (n > 0) {
+                            const Visible vis = visible_of(n, args.pos[t], args.window, args.sinks);
+                            hi[e] = vis.hi;
+                            lo[e] = vis.lo;
+                        }
+                    }
+                }
+            }
+            const bool more = walk.next(args, ws, nxt);
+            bool used = true;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = e * 32 + lane;
+                if (c >= N) continue;
+                const bool dead = hi[e] < 0 || v[e] == -INFINITY;
+                used = used && !dead;
+                cl[c] = dead ? 0.f : v[e] * 1.4426950408889634f;
+                ch[c] = dead ? -1 : hi[e];
+                co[c] = lo[e];
+            }
+            used = __all_sync(0xffffffffu, used);
+            if (el) {
+                const int k0 = cur.key0 + 128 * (int)rank;
+                StepInfo s;
+                s.N = N;
+                s.whole = used && cur.n > 0 && k0 + 127 <= cur.rg.min_hi &&
+                          (k0 >= cur.rg.max_lo || k0 + 128 <= sink_end);
+                s.last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
+                s.b = cur.b;
+                s.key0 = cur.key0;
+                s.part = cur.split ? cid * 2 + (cur.base < walk.w0 ? 0 : 1) : -1;
+                info[buf] = s;
+                if (rank == 0 && cur.split && s.last) {
+                    // the cluster of the tile's last step names it for the join
+                    const long long end = cur.base + kTileCost + steps_of(ws.seqs[cur.b], args.Hq);
+                    if (end <= walk.w1) {
+                        SplitTile d;
+                        d.b = cur.b;
+                        d.tile = cur.key0;
+                        d.c_first = (int)(((cur.base + kTileCost + 1) * walk.ncl - 1) / walk.total);
+                        d.c_last = cid;
+                        d.base = cur.base;
+                        d.pad = 0;
+                        ws.desc[cid] = d;
+                    }
+                }
+            }
+            __syncwarp();
+            if (el) mbar_arrive(bar(B_COL + buf));
+            cur = nxt;
+            have = more;
+            ++gd;
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------- sums
+        // TMEM lane i holds key i of this CTA's 128; hs takes half of the columns.
+        const int hs = warp >> 2;
+        const int i = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float* col_f = reinterpret_cast<const float*>(sgen + kOffCol);
+        const StepInfo* info = reinterpret_cast<const StepInfo*>(sgen + kOffStep);
+        float* half_s = reinterpret_cast<float*>(sgen + kOffHalf);
+        const uint32_t dfree0 = mapa(bar(B_DFREE), 0);
+        const int S = args.pg.max_pages * args.pg.page_size;
+        const int sink_end = args.window > 0 ? args.sinks : 0;
         int g = 0, tiles = 0;
         float sum = 0.f;
-        while (ok && have) {
-            const bool more = walk.next(args, ws, nxt);
-            const bool last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
-            const int key = cur.key0 + 128 * (int)rank + i;
-            if (cur.n > 0) {
+        for (int gd = 0;; ++gd) {
+            if (!wait_all(bar(B_COL + (gd & 1)), (gd >> 1) & 1, abort_flag, 2200, gd)) break;
+            const StepInfo st = info[gd & 1];
+            if (st.N < 0) break;
+            const int key = st.key0 + 128 * (int)rank + i;
+            if (st.N > 0) {
+                const float* cl = col_f + (gd & 1) * 3 * kPairs;
+                const int* ch = reinterpret_cast<const int*>(cl + kPairs);
+                const int* co = ch + kPairs;
                 const int buf = g & 1;
-                float* cl = col_f + buf * 3 * kPairs;
-                int* ch = reinterpret_cast<int*>(cl + kPairs);
-                int* co = ch + kPairs;
-                cl[tid] = c_lse;
-                ch[tid] = c_hi;
-                co[tid] = c_lo;
-                const bool used = __all_sync(0xffffffffu, c_hi >= 0);
-                if (lane == 0) plain_s[buf * 8 + warp] = used ? 1 : 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_COL + buf));
-                if (more && nxt.n > 0) fetch(nxt);
-                if (!wait_all(bar(B_COL + buf), (g >> 1) & 1, abort_flag, 2200, g)) { ok = false; break; }
-                const int N = n_of(cur);
-                const int k0 = cur.key0 + 128 * (int)rank;
-                bool whole = cur.rg.all && k0 + 127 <= cur.rg.min_hi && (k0 >= cur.rg.max_lo || k0 + 128 <= sink_end);
-                for (int w = 0; w < N / 32; ++w) whole = whole && plain_s[buf * 8 + w] != 0;
-                if (!wait_all(bar(B_DFULL + buf), (g >> 1) & 1, abort_flag, 2210, g)) { ok = false; break; }
+                if (!wait_all(bar(B_DFULL + buf), (g >> 1) & 1, abort_flag, 2210, g)) break;
                 tc_fence_after();
-                const int per = N / 2;
+                const int per = st.N / 2;
                 const uint32_t ta = tmem + lane_addr + (uint32_t)buf * 256 + hs * per;
                 float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll 1
@@ -589,7 +672,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                     tmem_ld32(ta + c0, d);
                     tmem_wait_ld();
                     const float4* l4 = reinterpret_cast<const float4*>(cl + hs * per + c0);
-                    if (whole) {
+                    if (st.whole) {
 #pragma unroll
                         for (int v = 0; v < 8; ++v) {
                             const float4 l = l4[v];
@@ -622,10 +705,8 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 // the loads' results are here, so the signal need not order them
                 if (lane == 0) mbar_arrive_remote_relaxed(dfree0 + 8u * (uint32_t)buf);
                 ++g;
-            } else if (more && nxt.n > 0) {
-                fetch(nxt);
             }
-            if (last) {
+            if (st.last) {
                 // both column halves of a key, then its sum
                 float* hv = half_s + (tiles & 1) * 128;
                 if (hs == 1) {
@@ -633,35 +714,19 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_HALF + (tiles & 1)));
                 } else {
-                    if (!wait_all(bar(B_HALF + (tiles & 1)), (tiles >> 1) & 1, abort_flag, 2220, g)) { ok = false; break; }
+                    if (!wait_all(bar(B_HALF + (tiles & 1)), (tiles >> 1) & 1, abort_flag, 2220, g)) break;
                     const float total = sum + hv[i];
-                    if (cur.split) {
-                        const int place = cur.base < walk.w0 ? 0 : 1;
-                        ws.parts[((size_t)cid * 2 + place) * kTile + 128 * rank + i] = total;
-                    } else if (key < S && total != 0.f) {
-                        mass[(size_t)cur.b * S + key] += total;
-                    }
-                }
-                if (rank == 0 && threadIdx.x == 0 && cur.split) {
-                    // the cluster of the tile's last step names it for the join
-                    const SeqPlan sp = ws.seqs[cur.b];
-                    const long long end = cur.base + kTileCost + steps_of(sp, args.Hq);
-                    if (end <= walk.w1) {
-                        SplitTile d;
-                        d.b = cur.b;
-                        d.tile = cur.key0;
-                        d.c_first = (int)(((cur.base + kTileCost + 1) * walk.ncl - 1) / walk.total);
-                        d.c_last = cid;
-                        d.base = cur.base;
-                        d.pad = 0;
-                        ws.desc[cid] = d;
-                    }
+                    if (st.part >= 0)
+                        ws.parts[(size_t)st.part * kTile + 128 * rank + i] = total;
+                    else if (key < S && total != 0.f)
+                        mass[(size_t)st.b * S + key] += total;
                 }
                 sum = 0.f;
                 ++tiles;
             }
-            cur = nxt;
-            have = more;
+            // last of all: the halves' buffer of two tiles ago is free by it, too
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_COLFREE + (gd & 1)));
         }
     }
 

@@ -1344,10 +1344,10 @@ int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_le
         return fail(DSA_ERR_ARG, "sinks=%d and recent=%d must be >= 0 and at most keep=%d together", sinks, recent,
                     keep);
     if (max_len > kMaxLen) return fail(DSA_ERR_UNSUPPORTED, "max_len=%d (supported: up to %d)", max_len, kMaxLen);
-    // the smallest cluster whose shared memory holds a row of weights, more CTAs
-    // where there are few sequences, at most 8
+    // the smallest cluster with at most kSelShare positions a CTA, more CTAs where
+    // there are few sequences, at most 8
     int size = 1;
-    while (size < kSelMaxCluster && ((long long)size * kSelRound < max_len ||
+    while (size < kSelMaxCluster && ((long long)size * kSelShare < max_len ||
                                      ((long long)n_seqs * size < num_sms() && size * 4096 < max_len)))
         size *= 2;
     if ((long long)n_seqs * size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
