@@ -18,9 +18,11 @@
 // of whose rows sees a key of the tile are passed over.
 //
 // Warps (11 per CTA): 0-7 sums (two per TMEM lane quarter, half of the columns
-// each), 8 loads, 9 MMA issue (even CTA), 10 the next step's columns (lse, keys
-// seen), a step ahead of the sums: with the sums' own loads in their loop a
-// step took 8500 clocks instead of MEASURED.
+// each), 8 loads, 9 MMA issue (even CTA), 10 the steps: it walks the piece and
+// hands each step, with its columns' lse and keys seen, to the others up to
+// four steps ahead. (Each warp walking for itself put 1400 to 1900 clocks of
+// load latency between two steps' MMAs, and the columns' loads 4000 between
+// two steps' sums: 256 rows over 12K keys took 505 us.)
 #pragma once
 #include <cuda.h>
 
@@ -48,15 +50,16 @@ constexpr int kQSlots = 4;
 constexpr int kOffK = 0;
 constexpr int kOffQ = kOffK + kSlabs * kKSlab;
 constexpr int kOffBar = kOffQ + kQSlots * kQSlot;
-constexpr int kOffCol = kOffBar + 512;                    // [2][256] lse2, last and first key seen
-constexpr int kOffHalf = kOffCol + 2 * 3 * kPairs * 4;    // [2][128] sums of the second column half
-constexpr int kOffStep = kOffHalf + 2 * 128 * 4;          // [2] StepInfo
-constexpr int kSmem = kOffStep + 2 * 64 + 1024;
+constexpr int kAhead = 4;                                 // steps handed out ahead
+constexpr int kOffCol = kOffBar + 512;                    // [kAhead][256] lse2, last and first key seen
+constexpr int kOffHalf = kOffCol + kAhead * 3 * kPairs * 4;   // [kAhead][128] sums of the second column half
+constexpr int kOffStep = kOffHalf + kAhead * 128 * 4;          // [kAhead] StepInfo
+constexpr int kSmem = kOffStep + kAhead * 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 
 enum : int {
-    B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_COL = 30, B_COLFREE = 32,
-    B_HALF = 34, B_DRAIN = 36, B_COUNT = 37
+    B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_STEP = 30,
+    B_STEPFREE = 34, B_HALF = 38, B_DRAIN = 42, B_COUNT = 43
 };
 
 constexpr int kMaxClusters = cache_attn::kMaxClusters;
@@ -136,22 +139,21 @@ __device__ __forceinline__ long long piece_begin(long long total, int ncl, int c
 
 constexpr int kPlanThreads = 1024;
 
+constexpr int kPlanSeqs = 1024;     // sequences that the plan handles in shared memory
+
 // One CTA: rows and keys of each sequence, then the line of work.
 __global__ void __launch_bounds__(kPlanThreads)
 cache_mass_plan_kernel(const Args a, int clusters, void* ws)
 {
     __shared__ long long wsum[32];
+    __shared__ SeqPlan near[kPlanSeqs];
     const Ws w = ws_of(ws);
+    volatile SeqPlan* seqs = a.pg.n_seqs <= kPlanSeqs ? near : w.seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     for (int b = tid; b < a.pg.n_seqs; b += kPlanThreads) {
-        SeqPlan s;
-        s.t_min = INT_MAX;
-        s.t_max = -1;
-        s.hi = -1;
-        s.lo = INT_MAX;
-        s.start = s.pad = 0;
-        w.seqs[b] = s;
+        seqs[b].t_min = seqs[b].lo = INT_MAX;
+        seqs[b].t_max = seqs[b].hi = -1;
     }
     for (int c = tid; c < clusters; c += kPlanThreads) w.desc[c].b = -1;
     __syncthreads();
@@ -182,10 +184,10 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
             mine = mine && lane == 0;
         }
         if (mine) {
-            atomicMin(&w.seqs[b].t_min, t_min);
-            atomicMax(&w.seqs[b].t_max, t_max);
-            atomicMax(&w.seqs[b].hi, hi);
-            atomicMin(&w.seqs[b].lo, lo);
+            atomicMin(const_cast<int*>(&seqs[b].t_min), t_min);
+            atomicMax(const_cast<int*>(&seqs[b].t_max), t_max);
+            atomicMax(const_cast<int*>(&seqs[b].hi), hi);
+            atomicMin(const_cast<int*>(&seqs[b].lo), lo);
         }
     }
     __syncthreads();
@@ -193,9 +195,9 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
     const int b0 = min(a.pg.n_seqs, tid * per), b1 = min(a.pg.n_seqs, b0 + per);
     auto cost = [&](int b) -> long long {
         SeqPlan s;
-        s.t_min = __ldcg(&w.seqs[b].t_min);
-        s.t_max = __ldcg(&w.seqs[b].t_max);
-        const Tiles k = tiles_of(__ldcg(&w.seqs[b].lo), __ldcg(&w.seqs[b].hi), sink_end);
+        s.t_min = seqs[b].t_min;
+        s.t_max = seqs[b].t_max;
+        const Tiles k = tiles_of(seqs[b].lo, seqs[b].hi, sink_end);
         return (long long)k.nt * (steps_of(s, a.Hq) + kTileCost);
     };
     long long sum = 0;
@@ -219,8 +221,19 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
         w.head->ncl = ncl;
     }
     for (int b = b0; b < b1; ++b) {
-        w.seqs[b].start = pre;
-        pre += cost(b);
+        const long long c = cost(b);
+        if (a.pg.n_seqs <= kPlanSeqs) {
+            SeqPlan s;
+            s.t_min = seqs[b].t_min;
+            s.t_max = seqs[b].t_max;
+            s.hi = seqs[b].hi;
+            s.lo = seqs[b].lo;
+            s.start = pre;
+            s.pad = 0;
+            w.seqs[b] = s;
+        }
+        seqs[b].start = pre;
+        pre += c;
     }
     __syncthreads();
     // the sequence in which each cluster's piece starts: the last one that starts
@@ -230,13 +243,21 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
         int l = 0, r = a.pg.n_seqs - 1;
         while (l < r) {
             const int m = (l + r + 1) / 2;
-            if (__ldcg(&w.seqs[m].start) <= w0)
+            if (seqs[m].start <= w0)
                 l = m;
             else
                 r = m - 1;
         }
         w.head->first[tid] = l;
     }
+}
+
+// What row t sees if it belongs to sequence b (false: nothing).
+__device__ __forceinline__ bool sees(const Args& a, int b, int t, Visible& v)
+{
+    const int sq = a.pg.seq[t], p = a.pos[t];
+    v = visible_of((int)min((long long)p + 1, (long long)a.pg.max_pages * a.pg.page_size), p, a.window, a.sinks);
+    return sq == b && p >= 0;
 }
 
 // Rows [t0, t0 + n) as a step of sequence b (a whole warp takes part): what
@@ -254,12 +275,8 @@ __device__ __forceinline__ StepRange step_range(const Args& a, int b, int t0, in
     r.max_lo = 0;
     bool all = true;
     for (int i = threadIdx.x & 31; i < n; i += 32) {
-        const int t = t0 + i;
-        long long base;
-        const int* bt;
-        const int k = a.pg.seq[t] == b ? row_keys(a.pg, a.pos, nullptr, t, a.T, 0, &base, &bt) : 0;
-        if (k > 0) {
-            const Visible v = visible_of(k, a.pos[t], a.window, a.sinks);
+        Visible v;
+        if (sees(a, b, t0 + i, v)) {
             r.hi = max(r.hi, v.hi);
             r.min_hi = min(r.min_hi, v.hi);
             r.lo = min(r.lo, v.lo);
@@ -285,14 +302,18 @@ struct Step {
     long long base;            // the tile's place on the line of work
 };
 
-// What the summing warps need to know of a step.
+// What the other warps need to know of a step.
 struct StepInfo {
     int N;          // columns; 0: no step, only a share's end; -1: no more
     int whole;      // every column sees each of this CTA's 128 keys
+    int seen;       // some column sees one of them
     int last;       // the last step of this cluster's share of the tile
+    int fresh;      // its first one
     int b, key0;
     int part;       // where its partial sums go, -1: the share is the whole tile
-    int pad[10];
+    int qrow;       // first (row, head) pair
+    int row[2];     // cache rows of this CTA's two blocks of 64 keys
+    int pad[5];
 };
 static_assert(sizeof(StepInfo) == 64, "StepInfo");
 
@@ -405,9 +426,11 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         for (int d = 0; d < 2; ++d) {
             mbar_init(bar(B_DFULL + d), 1);
             mbar_init(bar(B_DFREE + d), 16);    // the summing warps of both CTAs
-            mbar_init(bar(B_COL + d), 1);
-            mbar_init(bar(B_COLFREE + d), 8);
+        }
+        for (int d = 0; d < kAhead; ++d) {
+            mbar_init(bar(B_STEP + d), 1);
             mbar_init(bar(B_HALF + d), 4);
+            mbar_init(bar(B_STEPFREE + d), rank == 0 ? 10 : 9);   // sums, loads, MMA issue
         }
         mbar_init(bar(B_DRAIN), 1);
         *abort_flag = 0;
@@ -428,6 +451,15 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
     bool issued_any = false;
     // pairs of a step as the MMA's N
     auto n_of = [&](const Step& s) -> int { return s.n * args.Hq > 128 ? 256 : 128; };
+    // step gd for the loads' and the issuing warp, which need nothing more of it
+    auto take_step = [&](int gd, StepInfo& st) -> bool {
+        const int at = gd % kAhead;
+        if (!wait_lanes(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2050, gd)) return false;
+        st = reinterpret_cast<const StepInfo*>(sgen + kOffStep)[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_STEPFREE + at));
+        return true;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------------ loads
@@ -437,26 +469,17 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             prefetch_tmap(&tm_q64);
         }
         const uint32_t kfull0 = mapa(bar(B_KFULL), 0), qfull0 = mapa(bar(B_QFULL), 0);
-        int slot = 0, n_tiles = 0, last_b = -1, last_tile = -1;
+        int slot = 0, n_tiles = 0;
         uint32_t ph = 0;
         bool ok = true;
-        StepWalk walk(args, ws, cid);
-        Step st;
-        while (ok && walk.next(args, ws, st)) {
-            if (st.n == 0) continue;
-            const bool fresh = st.b != last_b || st.tile != last_tile;
-            int row0 = 0, row1 = 0;
-            if (fresh) {
-                last_b = st.b;
-                last_tile = st.tile;
-                // blocks of 64 keys behind the last key seen read that key's
-                const int* bt = args.pg.block_table + (size_t)st.b * args.pg.max_pages;
-                const int s0 = st.key0 + 128 * (int)rank, top = st.hi_b / 64 * 64;
-                row0 = (int)key_row(args.pg, bt, 0, min(s0, top));
-                row1 = (int)key_row(args.pg, bt, 0, min(s0 + 64, top));
-            }
-            const int N = n_of(st);
-            const int qrow = st.t0 * args.Hq + (int)rank * (N / 2);
+        for (int gd = 0; ok; ++gd) {
+            StepInfo st;
+            if (!(ok = take_step(gd, st))) break;
+            if (st.N < 0) break;
+            if (st.N == 0) continue;
+            const bool fresh = st.fresh != 0;
+            const int N = st.N;
+            const int qrow = st.qrow + (int)rank * (N / 2);
             for (int k = 0; k < kSlabs; ++k) {
                 // a fresh tile waits for its slab of keys, too
                 const bool two = fresh && lane == 1;
@@ -467,8 +490,8 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                     if (fresh) {
                         if (rank == 0) mbar_arrive_expect_tx(bar(B_KFULL + k), 2 * kKSlab);
                         const uint32_t dst = sbase + kOffK + k * kKSlab;
-                        tma_load_3d_pair(dst, &tm_kv, 0, row0, k, kfull0 + 8u * (uint32_t)k);
-                        tma_load_3d_pair(dst + kKSlab / 2, &tm_kv, 0, row1, k, kfull0 + 8u * (uint32_t)k);
+                        tma_load_3d_pair(dst, &tm_kv, 0, st.row[0], k, kfull0 + 8u * (uint32_t)k);
+                        tma_load_3d_pair(dst + kKSlab / 2, &tm_kv, 0, st.row[1], k, kfull0 + 8u * (uint32_t)k);
                     }
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_QFULL + slot), (uint32_t)N * 128u);
                     tma_load_3d_pair(sbase + kOffQ + slot * kQSlot, N == 256 ? &tm_q128 : &tm_q64, 0, qrow, k,
@@ -495,18 +518,13 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         int slot = 0, g = 0, n_tiles = 0;
         uint32_t ph = 0;
         bool ok = true;
-        StepWalk walk(args, ws, cid);
-        Step cur, nxt;
-        auto advance = [&](Step& s) -> bool {
-            while (walk.next(args, ws, s))
-                if (s.n > 0) return true;
-            return false;
-        };
-        bool have = advance(cur), fresh = true;
-        while (ok && have) {
-            const bool more = advance(nxt);
-            const bool last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
-            const uint32_t idesc = n_of(cur) == 256 ? idesc_bf16(256, 256, false) : idesc_bf16(256, 128, false);
+        for (int gd = 0; ok; ++gd) {
+            StepInfo st;
+            if (!(ok = take_step(gd, st))) break;
+            if (st.N < 0) break;
+            if (st.N == 0) continue;
+            const bool fresh = st.fresh != 0, last = st.last != 0;
+            const uint32_t idesc = st.N == 256 ? idesc_bf16(256, 256, false) : idesc_bf16(256, 128, false);
             const uint32_t d = tmem + (uint32_t)(g & 1) * 256;
             for (int k = 0; k < kSlabs && ok; ++k) {
                 // lane 0: Q, lane 1: the keys of a fresh tile, lane 2: D read (step g - 2)
@@ -537,72 +555,75 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             if (!ok) break;
             mma_commit_pair(bar(B_DFULL + (g & 1)), el);
             if (last) ++n_tiles;
-            fresh = last;
             ++g;
-            cur = nxt;
-            have = more;
         }
     } else if (warp == 10) {
-        // ------------------------------------------- columns of the steps
+        // ----------------------------------------------------------- steps
         float* col_f = reinterpret_cast<float*>(sgen + kOffCol);
         StepInfo* info = reinterpret_cast<StepInfo*>(sgen + kOffStep);
         const int sink_end = args.window > 0 ? args.sinks : 0;
-        int gd = 0;
+        int gd = 0, b_prev = -1, tile_prev = -1, row0 = 0, row1 = 0;
         bool ok = true;
         StepWalk walk(args, ws, cid);
         Step cur, nxt;
         bool have = walk.next(args, ws, cur);
         while (ok) {
-            const int buf = gd & 1;
-            ok = wait_lanes(bar(B_COLFREE + buf), (uint32_t)(((gd >> 1) & 1) ^ 1), abort_flag, 2300, gd);
+            const int buf = gd % kAhead;
+            ok = wait_lanes(bar(B_STEPFREE + buf), (uint32_t)(((gd / kAhead) & 1) ^ 1), abort_flag, 2300, gd);
             if (!ok) break;
             if (!have) {
                 if (el) {
                     info[buf].N = -1;
-                    mbar_arrive(bar(B_COL + buf));
+                    mbar_arrive(bar(B_STEP + buf));
                 }
                 break;
             }
             float* cl = col_f + buf * 3 * kPairs;
             int* ch = reinterpret_cast<int*>(cl + kPairs);
             int* co = ch + kPairs;
-            const int N = cur.n > 0 ? n_of(cur) : 0;
+            const int N = cur.n > 0 ? n_of(cur) : 0, cols = cur.n * args.Hq;
             // a column's lse and the keys that its row sees (none: a column without a
             // row of this sequence, or with nothing to give)
             float v[8];
-            int hi[8], lo[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = e * 32 + lane;
-                hi[e] = -1;
-                lo[e] = 0;
-                v[e] = -INFINITY;
-                if (c < cur.n * args.Hq) {
-                    const int t = cur.t0 + c / args.Hq;
-                    v[e] = __ldg(lse + (size_t)cur.t0 * args.Hq + c);
-                    if (args.pg.seq[t] == cur.b) {
-                        long long base;
-                        const int* bt;
-                        const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
-                        if (n > 0) {
-                            const Visible vis = visible_of(n, args.pos[t], args.window, args.sinks);
-                            hi[e] = vis.hi;
-                            lo[e] = vis.lo;
-                        }
-                    }
-                }
+                v[e] = c < cols ? __ldg(lse + (size_t)cur.t0 * args.Hq + c) : -INFINITY;
             }
+            const bool fresh = cur.n > 0 && (cur.b != b_prev || cur.tile != tile_prev);
+            if (fresh) {
+                b_prev = cur.b;
+                tile_prev = cur.tile;
+                // blocks of 64 keys behind the last key seen read that key's
+                const int* bt = args.pg.block_table + (size_t)cur.b * args.pg.max_pages;
+                const int s0 = cur.key0 + 128 * (int)rank, top = cur.hi_b / 64 * 64;
+                row0 = (int)key_row(args.pg, bt, 0, min(s0, top));
+                row1 = (int)key_row(args.pg, bt, 0, min(s0 + 64, top));
+            }
+            // a row's keys in its lane; more rows than lanes (fewer than 8 heads): in their columns' lanes
+            Visible mine;
+            bool live = false;
+            if (lane < cur.n) live = sees(args, cur.b, cur.t0 + lane, mine);
             const bool more = walk.next(args, ws, nxt);
             bool used = true;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int c = e * 32 + lane;
+                const int c = e * 32 + lane, r = min(c / args.Hq, max(cur.n, 1) - 1);
+                Visible w;
+                bool l;
+                if (cur.n <= 32) {
+                    w.hi = __shfl_sync(0xffffffffu, mine.hi, r);
+                    w.lo = __shfl_sync(0xffffffffu, mine.lo, r);
+                    l = __shfl_sync(0xffffffffu, live ? 1 : 0, r) != 0;
+                } else {
+                    l = sees(args, cur.b, cur.t0 + r, w);
+                }
                 if (c >= N) continue;
-                const bool dead = hi[e] < 0 || v[e] == -INFINITY;
+                const bool dead = c >= cols || !l || v[e] == -INFINITY;
                 used = used && !dead;
                 cl[c] = dead ? 0.f : v[e] * 1.4426950408889634f;
-                ch[c] = dead ? -1 : hi[e];
-                co[c] = lo[e];
+                ch[c] = dead ? -1 : w.hi;
+                co[c] = w.lo;
             }
             used = __all_sync(0xffffffffu, used);
             if (el) {
@@ -611,10 +632,15 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 s.N = N;
                 s.whole = used && cur.n > 0 && k0 + 127 <= cur.rg.min_hi &&
                           (k0 >= cur.rg.max_lo || k0 + 128 <= sink_end);
+                s.seen = cur.n > 0 && k0 <= cur.rg.hi && (k0 + 128 > cur.rg.lo || k0 < sink_end);
                 s.last = !more || nxt.b != cur.b || nxt.tile != cur.tile;
+                s.fresh = fresh;
                 s.b = cur.b;
                 s.key0 = cur.key0;
                 s.part = cur.split ? cid * 2 + (cur.base < walk.w0 ? 0 : 1) : -1;
+                s.qrow = cur.t0 * args.Hq;
+                s.row[0] = row0;
+                s.row[1] = row1;
                 info[buf] = s;
                 if (rank == 0 && cur.split && s.last) {
                     // the cluster of the tile's last step names it for the join
@@ -632,7 +658,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 }
             }
             __syncwarp();
-            if (el) mbar_arrive(bar(B_COL + buf));
+            if (el) mbar_arrive(bar(B_STEP + buf));
             cur = nxt;
             have = more;
             ++gd;
@@ -649,15 +675,17 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         const uint32_t dfree0 = mapa(bar(B_DFREE), 0);
         const int S = args.pg.max_pages * args.pg.page_size;
         const int sink_end = args.window > 0 ? args.sinks : 0;
+        const bool windowed = args.window > 0;
         int g = 0, tiles = 0;
         float sum = 0.f;
         for (int gd = 0;; ++gd) {
-            if (!wait_all(bar(B_COL + (gd & 1)), (gd >> 1) & 1, abort_flag, 2200, gd)) break;
-            const StepInfo st = info[gd & 1];
+            const int at = gd % kAhead;
+            if (!wait_all(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2200, gd)) break;
+            const StepInfo st = info[at];
             if (st.N < 0) break;
             const int key = st.key0 + 128 * (int)rank + i;
             if (st.N > 0) {
-                const float* cl = col_f + (gd & 1) * 3 * kPairs;
+                const float* cl = col_f + at * 3 * kPairs;
                 const int* ch = reinterpret_cast<const int*>(cl + kPairs);
                 const int* co = ch + kPairs;
                 const int buf = g & 1;
@@ -667,7 +695,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 const uint32_t ta = tmem + lane_addr + (uint32_t)buf * 256 + hs * per;
                 float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll 1
-                for (int c0 = 0; c0 < per; c0 += 32) {
+                for (int c0 = 0; c0 < per && st.seen; c0 += 32) {
                     uint32_t d[32];
                     tmem_ld32(ta + c0, d);
                     tmem_wait_ld();
@@ -682,20 +710,34 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                             acc1 += ex2(fmaf(__uint_as_float(d[4 * v + 3]), scale_log2, -l.w));
                         }
                     } else {
+                        // only the keys that a column's row sees; without a window all of them
+                        // from 0 on
                         const int4* h4 = reinterpret_cast<const int4*>(ch + hs * per + c0);
                         const int4* o4 = reinterpret_cast<const int4*>(co + hs * per + c0);
-                        auto term = [&](uint32_t x, float l, int h, int o) -> float {
-                            const bool seen = key <= h && (key >= o || key < sink_end);
-                            return seen ? ex2(fmaf(__uint_as_float(x), scale_log2, -l)) : 0.f;
+                        auto add = [&](float& acc, uint32_t x, float l, bool seen) {
+                            const float p = ex2(fmaf(__uint_as_float(x), scale_log2, -l));
+                            if (seen) acc += p;
                         };
+                        if (key < sink_end || !windowed) {
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            const float4 l = l4[v];
-                            const int4 h = h4[v], o = o4[v];
-                            acc0 += term(d[4 * v], l.x, h.x, o.x);
-                            acc1 += term(d[4 * v + 1], l.y, h.y, o.y);
-                            acc0 += term(d[4 * v + 2], l.z, h.z, o.z);
-                            acc1 += term(d[4 * v + 3], l.w, h.w, o.w);
+                            for (int v = 0; v < 8; ++v) {
+                                const float4 l = l4[v];
+                                const int4 h = h4[v];
+                                add(acc0, d[4 * v], l.x, key <= h.x);
+                                add(acc1, d[4 * v + 1], l.y, key <= h.y);
+                                add(acc0, d[4 * v + 2], l.z, key <= h.z);
+                                add(acc1, d[4 * v + 3], l.w, key <= h.w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < 8; ++v) {
+                                const float4 l = l4[v];
+                                const int4 h = h4[v], o = o4[v];
+                                add(acc0, d[4 * v], l.x, key <= h.x && key >= o.x);
+                                add(acc1, d[4 * v + 1], l.y, key <= h.y && key >= o.y);
+                                add(acc0, d[4 * v + 2], l.z, key <= h.z && key >= o.z);
+                                add(acc1, d[4 * v + 3], l.w, key <= h.w && key >= o.w);
+                            }
                         }
                     }
                 }
@@ -708,13 +750,13 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             }
             if (st.last) {
                 // both column halves of a key, then its sum
-                float* hv = half_s + (tiles & 1) * 128;
+                float* hv = half_s + tiles % kAhead * 128;
                 if (hs == 1) {
                     hv[i] = sum;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_HALF + (tiles & 1)));
+                    if (lane == 0) mbar_arrive(bar(B_HALF + tiles % kAhead));
                 } else {
-                    if (!wait_all(bar(B_HALF + (tiles & 1)), (tiles >> 1) & 1, abort_flag, 2220, g)) break;
+                    if (!wait_all(bar(B_HALF + tiles % kAhead), (tiles / kAhead) & 1, abort_flag, 2220, g)) break;
                     const float total = sum + hv[i];
                     if (st.part >= 0)
                         ws.parts[(size_t)st.part * kTile + 128 * rank + i] = total;
@@ -724,9 +766,9 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 sum = 0.f;
                 ++tiles;
             }
-            // last of all: the halves' buffer of two tiles ago is free by it, too
+            // last of all: a tile's buffer of half sums is free by it, too
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_COLFREE + (gd & 1)));
+            if (lane == 0) mbar_arrive(bar(B_STEPFREE + at));
         }
     }
 
