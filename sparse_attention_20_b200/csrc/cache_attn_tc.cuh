@@ -31,8 +31,10 @@
 // an infinity, 0 times which would reach every row, those are zeroed in
 // shared memory before PV (a row that does see the key has a NaN logit).
 //
-// Warps (10 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
-// keys each), Q, epilogue; 8 loads; 9 MMA issue (even CTA).
+// Warps (16 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
+// keys each) and Q; 8 loads; 9 MMA issue (even CTA); 10 walks the cluster's
+// piece and hands its parts to the others; 12-15 take O out of TMEM and write
+// it, while the softmax is at the next unit already.
 #pragma once
 #include <cuda.h>
 
@@ -46,7 +48,8 @@ using namespace sm100;
 
 constexpr int kRows = 128;                 // (row, head) pairs of a unit
 constexpr int kTile = 128;                 // keys of a tile
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 512;
+constexpr int kPlanWarps = kTcThreads / 32;
 constexpr int kSlab = 64 * 128;            // 64 rows x 64 columns bf16, 128B swizzle
 constexpr int kSlotBytes = 4 * kSlab;
 constexpr int kSlots = 5;
@@ -58,20 +61,24 @@ constexpr int kOffRing = kOffRope + 2 * kSlab;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
 constexpr int kOffRed = kOffBar + 512;                // [2][4][64] row maxima
 constexpr int kOffLsum = kOffRed + 2 * 4 * 64 * 4;    // [2][4][64] row sums
-constexpr int kOffBad = kOffLsum + 2 * 4 * 64 * 4;    // [2][8] flags of the softmax warps
-constexpr int kOffPlan = kOffBad + 64;
+constexpr int kOffMax = kOffLsum + 2 * 4 * 64 * 4;    // [2][64] row maxima that the sums refer to
+constexpr int kOffBad = kOffMax + 2 * 64 * 4;         // [2][8] flags of the softmax warps
+constexpr int kAhead = 4;                             // parts handed out ahead
+constexpr int kOffParts = kOffBad + 64;               // [kAhead] PartInfo
+constexpr int kOffPlan = kOffParts + kAhead * 64;
 constexpr int kTcSmem = kOffPlan + 256 + 1024;        // + alignment slack
 static_assert(kTcSmem <= 232448, "shared memory");
 
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
 // On the even CTA's barriers: FULL, RFULL (bytes of both CTAs), QT, SFREE, PFULL
-// (arrivals of both). OWN: a slot that the softmax warps look at first (a unit's
+// OFREE (arrivals of both). OWN: a slot that the softmax warps look at first (a unit's
 // Q, the values of a tile that not every row sees whole), QROPE: Q's last
 // slab, on each CTA's own.
 enum : int {
     B_FULL = 0, B_EMPTY = 5, B_OWN = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
-    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QROPE = 28, B_COUNT = 29
+    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QROPE = 28,
+    B_OFREE = 29, B_PART = 30, B_PARTFREE = 34, B_COUNT = 38
 };
 
 constexpr int kMaxClusters = 74;
@@ -100,17 +107,18 @@ struct Args {
     int T, Hq, window, sinks;
 };
 
+// What a row of sequence sq at position p sees (false: nothing).
+__device__ __forceinline__ bool row_sees(const Args& a, int sq, int p, Visible& v)
+{
+    v = visible_of((int)min((long long)p + 1, (long long)a.pg.max_pages * a.pg.page_size), p, a.window, a.sinks);
+    return sq >= 0 && sq < a.pg.n_seqs && p >= 0;
+}
+
 // Rows t .. t + n - 1 of one sequence and the tiles of keys that they see.
 struct Unit {
     int t, n, hi, min_hi, max_lo, sink_end;
     int ns, m0, nt;                // sink tiles, first tile after them, tiles in all
     const int* bt;
-    __device__ __forceinline__ int key0(int i) const { return (i < ns ? i : m0 + i - ns) * kTile; }
-    // every row sees keys [s, s + m)
-    __device__ __forceinline__ bool all_see(int s, int m) const
-    {
-        return s + m - 1 <= min_hi && (s >= max_lo || s + m <= sink_end);
-    }
 };
 
 __device__ __forceinline__ int rows_per_unit(int Hq) { return kRows / Hq; }
@@ -141,23 +149,23 @@ __device__ __forceinline__ Unit unit_at(const Args& a, int t)
     u.max_lo = 0;
     u.sink_end = a.window > 0 ? a.sinks : 0;
     for (int g0 = 0; g0 < G; g0 += lanes) {
-        const int r = t + g0 + lane;
-        const bool in = g0 + lane < G && r < a.T && a.pg.seq[r] == sq;
+        const int r = min(t + g0 + lane, a.T - 1);
+        const int sr = a.pg.seq[r], pr = a.pos[r];
+        const bool in = g0 + lane < G && t + g0 + lane < a.T && sr == sq;
         int cnt = in ? 1 : 0;
         if (lanes == 32) {
             const unsigned m = __ballot_sync(0xffffffffu, in);
             cnt = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
         }
         if (lane < cnt) {
-            long long base;
-            const int* bt;
-            const int n = row_keys(a.pg, a.pos, nullptr, r, a.T, 0, &base, &bt);
-            u.min_hi = min(u.min_hi, n - 1);
-            if (n > 0) {
-                const Visible v = visible_of(n, a.pos[r], a.window, a.sinks);
+            Visible v;
+            if (row_sees(a, sr, pr, v)) {
                 u.hi = max(u.hi, v.hi);
+                u.min_hi = min(u.min_hi, v.hi);
                 u.max_lo = max(u.max_lo, v.lo);
                 lo_min = min(lo_min, v.lo);
+            } else {
+                u.min_hi = -1;
             }
         }
         u.n += cnt;
@@ -174,22 +182,27 @@ __device__ __forceinline__ Unit unit_at(const Args& a, int t)
     return u;
 }
 
+// v / d, in 32 bits where they hold v (a 64-bit division takes some 150 clocks).
+__device__ __forceinline__ long long quotient(long long v, long long d)
+{
+    return ((v | d) >> 32) == 0 ? (long long)((uint32_t)v / (uint32_t)d) : v / d;
+}
+
 // This cluster's piece [w0, w1) of the line of work, and the unit it starts in.
 struct Piece {
     long long w0, w1, total, first_start;
     int first_t, ncl;
-    __device__ __forceinline__ int cluster_of(long long x) const { return (int)(((x + 1) * ncl - 1) / total); }
-    __device__ __forceinline__ static long long begin(long long total, int ncl, int c) { return total * c / ncl; }
+    __device__ __forceinline__ int cluster_of(long long x) const { return (int)quotient((x + 1) * ncl - 1, total); }
+    __device__ __forceinline__ static long long begin(long long total, int ncl, int c) { return quotient(total * c, ncl); }
 };
 
 // Block-wide: finds the units' places on the line of work from seq and pos
 // (every CTA does so for itself; a row costs a thread a few loads).
 __device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
 {
-    long long* s64 = reinterpret_cast<long long*>(smem);       // [10] warp sums, then the piece
-    int* s32 = reinterpret_cast<int*>(smem + 128);             // [10] last run start of each warp's rows
+    long long* s64 = reinterpret_cast<long long*>(smem);       // [16] warp sums, then the piece
+    int* s32 = reinterpret_cast<int*>(smem + 128);             // [16] last run start of each warp's rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kWarps = kTcThreads / 32;
     const int G = rows_per_unit(a.Hq);
     const int per = ceil_div(a.T, kTcThreads);
     const int r0 = min(a.T, tid * per), r1 = min(a.T, r0 + per);
@@ -229,7 +242,7 @@ __device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
     Piece p;
     p.total = 0;
     long long base = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kPlanWarps; ++w) {
         if (w < warp) base += s64[w];
         p.total += s64[w];
     }
@@ -262,7 +275,6 @@ struct Part {
     long long start;
     int a, b;
     bool owns_empty;       // a unit without keys, to be written as zeros
-    __device__ __forceinline__ bool split() const { return a > 0 || b < u.nt; }
 };
 
 // Walks the parts of a piece (a whole warp takes part).
@@ -286,6 +298,25 @@ struct Walk {
         return false;
     }
 };
+
+// A part as the other warps need it.
+struct PartInfo {
+    int t, rows;               // first row, (row, head) pairs
+    int hi, min_hi, max_lo, sink_end;
+    int ns, m0;
+    int a, nt;                 // first tile and tiles of the part; nt = 0: a unit without keys, -1: no more parts
+    int place;                 // its slot among the workspace's parts, -1: the part is the whole unit
+    int pad;
+    const int* bt;
+    long long pad2;
+    __device__ __forceinline__ int key0(int j) const { return (a + j < ns ? a + j : m0 + a + j - ns) * kTile; }
+    // every row sees keys [s, s + m)
+    __device__ __forceinline__ bool all_see(int s, int m) const
+    {
+        return s + m - 1 <= min_hi && (s >= max_lo || s + m <= sink_end);
+    }
+};
+static_assert(sizeof(PartInfo) == 64, "PartInfo");
 
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
 {
@@ -343,7 +374,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cid = (int)(blockIdx.x >> 1), clusters = (int)(gridDim.x >> 1);
+    const uint32_t el = elect_one();
 
+    griddep_launch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(bar(B_FULL + s), 1);
@@ -359,11 +392,16 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         mbar_init(bar(B_QT), 16);
         mbar_init(bar(B_SFREE), 16);
         mbar_init(bar(B_PFULL), 16);
+        mbar_init(bar(B_OFREE), 8);             // the warps that read O, of both CTAs
         mbar_init(bar(B_SFULL), 1);
         mbar_init(bar(B_PVDONE), 1);
         mbar_init(bar(B_LSUM), 8);
         mbar_init(bar(B_DRAIN), 1);
         mbar_init(bar(B_QROPE), 1);
+        for (int p = 0; p < kAhead; ++p) {
+            mbar_init(bar(B_PART + p), 1);
+            mbar_init(bar(B_PARTFREE + p), rank == 0 ? 14 : 13);   // softmax, loads, MMA issue, O
+        }
         *abort_flag = 0;
         fence_mbar_init_cluster();
     }
@@ -371,32 +409,40 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         tmem_alloc_pair(smem_u32(taddr_slot), 512);
         tmem_relinquish_pair();
     }
-    griddep_wait();
-    const Piece pc = plan(args, cid, clusters, sgen + kOffPlan);
+    if (warp == 8 && el) {
+        prefetch_tmap(&tm_kv4);
+        prefetch_tmap(&tm_kv1);
+        prefetch_tmap(&tm_q4);
+        prefetch_tmap(&tm_q1);
+    }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // the other CTA's barriers exist before any remote arrival
+    cluster_arrive();     // the other CTA's barriers exist before any remote arrival
+    griddep_wait();
+    const Piece pc = plan(args, cid, clusters, sgen + kOffPlan);
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = *taddr_slot;
     bool issued_any = false;
-
-    const uint32_t el = elect_one();
+    PartInfo* infos = reinterpret_cast<PartInfo*>(sgen + kOffParts);
+    // part n of the piece (false: given up); it is handed back at once
+    auto take_part = [&](int n, PartInfo& p) -> bool {
+        const int at = n % kAhead;
+        if (!wait_lanes(bar(B_PART + at), (n / kAhead) & 1, abort_flag, 1050, n)) return false;
+        p = infos[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PARTFREE + at));
+        return true;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------------ loads
-        if (el) {
-            prefetch_tmap(&tm_kv4);
-            prefetch_tmap(&tm_kv1);
-            prefetch_tmap(&tm_q4);
-            prefetch_tmap(&tm_q1);
-            if (rank == 0) desc[cid].n_rows = 0;
-        }
         int slot = 0, rslot = 0, n = 0;
         uint32_t ph = 0, rph = 0;
         bool ok = true;
         const uint32_t full0 = mapa(bar(B_FULL), 0), rfull0 = mapa(bar(B_RFULL), 0);
-        // one box of four slabs (columns 64 * z ..) of 64 cache rows from `row`;
-        // for own, the softmax warps wait for it and the MMA for them
+        // one box of four slabs (columns 64 * z ..) of 64 rows from `row`; for own
+        // the softmax warps wait for it and the MMA for them
         auto push = [&](const CUtensorMap* tm, int row, int z, bool own) {
             if (!ok) return;
             ok = wait_lanes(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, n);
@@ -438,51 +484,38 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             rslot ^= 1;
             if (rslot == 0) rph ^= 1u;
         };
-        Walk walk(pc);
-        Part p;
-        while (ok && walk.next(args, pc, p)) {
-            if (p.a >= p.b) continue;
+        PartInfo p;
+        for (int np = 0; ok; ++np) {
+            if (!(ok = take_part(np, p)) || p.nt < 0) break;
+            if (p.nt == 0) continue;
             // this CTA's 64 of the unit's pairs (rows behind the last are read as zeros)
-            const int qrow = p.u.t * args.Hq + (int)rank * 64;
+            const int qrow = p.t * args.Hq + (int)rank * 64;
             push(&tm_q4, qrow, 0, true);
             push(&tm_q4, qrow, 4, true);
             push_rope(&tm_q1, qrow, true);
-            if (rank == 0 && el && p.b == p.u.nt && p.a > 0) {
-                SplitDesc d;
-                d.t = p.u.t;
-                d.n_rows = p.u.n * args.Hq;
-                d.c_first = pc.cluster_of(p.start + kUnitCost);
-                d.c_last = cid;
-                d.start = p.start;
-                d.total = pc.total;
-                d.ncl = pc.ncl;
-                d.pad = 0;
-                desc[cid] = d;
-            }
             // cache rows of the tiles' two blocks of 64 keys, sixteen tiles at a
             // time over the lanes (a block behind the last key reads the one before)
             int rows_l = 0, pa = 0, pb = 0;
             bool pcut = false;
-            for (int j = p.a; j < p.b && ok; ++j, ++n) {
-                if (((j - p.a) & 15) == 0) {
-                    const int jj = min(j + (lane >> 1), p.b - 1);
-                    int s = p.u.key0(jj) + (lane & 1) * 64;
-                    if (s > p.u.hi) s -= 64;
-                    rows_l = (int)key_row(args.pg, p.u.bt, 0, s);
+            for (int j = 0; j < p.nt && ok; ++j, ++n) {
+                if ((j & 15) == 0) {
+                    int s = p.key0(min(j + (lane >> 1), p.nt - 1)) + (lane & 1) * 64;
+                    if (s > p.hi) s -= 64;
+                    rows_l = (int)key_row(args.pg, p.bt, 0, s);
                 }
-                const int e = ((j - p.a) & 15) * 2;
+                const int e = (j & 15) * 2;
                 const int ra = __shfl_sync(0xffffffffu, rows_l, e), rb = __shfl_sync(0xffffffffu, rows_l, e + 1);
-                const bool cut = !p.u.all_see(p.u.key0(j), kTile);
+                const bool cut = !p.all_see(p.key0(j), kTile);
                 const int own = rank ? rb : ra;
                 push(&tm_kv4, own, 0, false);
                 push(&tm_kv4, own, 4, false);
                 push_rope(&tm_kv1, own, false);
                 const int z = 4 * (int)rank;
-                if (j > p.a) {
+                if (j > 0) {
                     push(&tm_kv4, pa, z, pcut);
                     push(&tm_kv4, pb, z, pcut);
                 }
-                if (j == p.b - 1) {
+                if (j == p.nt - 1) {
                     push(&tm_kv4, ra, z, cut);
                     push(&tm_kv4, rb, z, cut);
                 }
@@ -508,10 +541,18 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         int slot = 0, rslot = 0, g = 0, n_units = 0;
         uint32_t ph = 0, rph = 0;
         bool ok = true;
-        // lane 0 waits for the slot, lane 1 for another barrier (par > 1: none)
-        auto ready = [&](int other, uint32_t par, int tag) -> bool {
-            const bool two = lane == 1 && par <= 1u;
-            return wait_lanes(two ? bar(other) : bar(B_FULL + slot), two ? par : ph, abort_flag, tag, g);
+        // lane 0 waits for the slot, lanes 1 and 2 for other barriers (par > 1: none)
+        auto ready = [&](int other, uint32_t par, int tag, int third = 0, uint32_t par3 = 2u) -> bool {
+            uint32_t wb = bar(B_FULL + slot), wp = ph;
+            if (lane == 1 && par <= 1u) {
+                wb = bar(other);
+                wp = par;
+            }
+            if (lane == 2 && par3 <= 1u) {
+                wb = bar(third);
+                wp = par3;
+            }
+            return wait_lanes(wb, wp, abort_flag, tag, g);
         };
         auto done = [&]() {
             mma_commit_pair(bar(B_EMPTY + slot), el);
@@ -552,11 +593,13 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             mma_commit_pair(bar(B_SFULL), el);
             return true;
         };
-        // O (+)= P C[:, 0:512] of tile gp
+        // O (+)= P C[:, 0:512] of tile gp; a unit's first waits until the last unit's O is read
         auto pv = [&](int gp, bool first) -> bool {
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
-                if (!ready(B_PFULL, blk == 0 ? (uint32_t)(gp & 1) : 2u, 1240)) return false;
+                if (!ready(B_PFULL, blk == 0 ? (uint32_t)(gp & 1) : 2u, 1240, B_OFREE,
+                           blk == 0 && first && n_units > 0 ? (uint32_t)((n_units - 1) & 1) : 2u))
+                    return false;
                 tc_fence_after();
                 const uint64_t b = d_v + (uint64_t)(slot * (kSlotBytes >> 4));
 #pragma unroll
@@ -571,10 +614,10 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             mma_commit_pair(bar(B_PVDONE), el);
             return true;
         };
-        Walk walk(pc);
-        Part p;
-        while (ok && walk.next(args, pc, p)) {
-            if (p.a >= p.b) continue;
+        PartInfo p;
+        for (int np = 0; ok; ++np) {
+            if (!(ok = take_part(np, p)) || p.nt < 0) break;
+            if (p.nt == 0) continue;
             ok = wait_lanes(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
             // the softmax warps have taken Q out of its two slots and rope slot
             done();
@@ -582,21 +625,143 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             mma_commit_pair(bar(B_REMPTY + rslot), el);
             rslot ^= 1;
             if (rslot == 0) rph ^= 1u;
-            const int nt = p.b - p.a;
-            for (int j = 0; j < nt && ok; ++j) {
+            for (int j = 0; j < p.nt && ok; ++j) {
                 ok = qk();
                 issued_any = true;
                 ++g;
                 if (ok && j > 0) ok = pv(g - 2, j == 1);
             }
-            if (ok) ok = pv(g - 1, nt == 1);
+            if (ok) ok = pv(g - 1, p.nt == 1);
             ++n_units;
         }
+    } else if (warp == 10) {
+        // ------------------------------------------------------------ parts
+        if (rank == 0 && el) desc[cid].n_rows = 0;
+        Walk walk(pc);
+        Part p;
+        bool more = true;
+        for (int np = 0; more; ++np) {
+            const int at = np % kAhead;
+            more = walk.next(args, pc, p);
+            if (!wait_lanes(bar(B_PARTFREE + at), (uint32_t)(((np / kAhead) & 1) ^ 1), abort_flag, 1060, np)) break;
+            if (el) {
+                PartInfo i;
+                i.t = p.u.t;
+                i.rows = p.u.n * args.Hq;
+                i.hi = p.u.hi;
+                i.min_hi = p.u.min_hi;
+                i.max_lo = p.u.max_lo;
+                i.sink_end = p.u.sink_end;
+                i.ns = p.u.ns;
+                i.m0 = p.u.m0;
+                i.a = p.a;
+                i.nt = more ? p.b - p.a : -1;
+                i.place = p.a > 0 || p.b < p.u.nt ? cid * 2 + (p.start < pc.w0 ? 0 : 1) : -1;
+                i.pad = 0;
+                i.bt = p.u.bt;
+                i.pad2 = 0;
+                infos[at] = i;
+                mbar_arrive(bar(B_PART + at));
+                if (more && rank == 0 && p.b == p.u.nt && p.a > 0) {
+                    SplitDesc d;
+                    d.t = p.u.t;
+                    d.n_rows = p.u.n * args.Hq;
+                    d.c_first = pc.cluster_of(p.start + kUnitCost);
+                    d.c_last = cid;
+                    d.start = p.start;
+                    d.total = pc.total;
+                    d.ncl = pc.ncl;
+                    d.pad = 0;
+                    desc[cid] = d;
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 12) {
+        // ---------------------------------------------------------- O out
+        // lane i holds pair i % 64 of this CTA's 64: columns 0..255 for i < 64, the
+        // others for i >= 64
+        const int i = (warp & 3) * 32 + lane, side = i >> 6, lr = i & 63;
+        const int r = (int)rank * 64 + lr;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float* lsum_s = reinterpret_cast<const float*>(sgen + kOffLsum);
+        const float* max_s = reinterpret_cast<const float*>(sgen + kOffMax);
+        const uint32_t ofree0 = mapa(bar(B_OFREE), 0);
+        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+        PartInfo p;
+        int uc = 0, g = 0;
+        for (int np = 0;; ++np) {
+            if (!take_part(np, p) || p.nt < 0) break;
+            const bool live = r < p.rows;
+            const size_t row = (size_t)p.t * args.Hq + r;
+            __nv_bfloat16* orow = out + row * kDv + side * 256;
+            if (p.nt == 0) {
+                if (live) {
+                    for (int v = 0; v < 32; ++v) reinterpret_cast<uint4*>(orow)[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (side == 0) lse[row] = -INFINITY;
+                }
+                __syncwarp();
+                continue;
+            }
+            g += p.nt;
+            // row sum over the four threads of the row
+            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g)) break;
+            const float* ls = lsum_s + (uc & 1) * 256 + lr;
+            const float l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
+            const float m = max_s[(uc & 1) * 64 + lr];
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const float lv = l != 0.f ? m + __log2f(l) : -INFINITY;
+            if (!wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1350, g)) break;
+            tc_fence_after();
+            float4* po = reinterpret_cast<float4*>(part_o) + (size_t)max(p.place, 0) * kRows * (kDv / 4) + r;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_addr + kColO + c0, o);
+                tmem_wait_ld();
+                if (live && p.place >= 0) {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        po[(size_t)((side * 256 + c0) / 4 + v) * kRows] =
+                            make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                        __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+                } else if (live) {
+                    // whole 32-byte sectors where out allows it
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv,
+                                               __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
+                        if (wide) {
+                            st_global_v8(orow + c0 + 16 * v, w);
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(orow + c0 + 16 * v);
+                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // the loads' results are here, so the signal need not order them
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(ofree0);
+            if (live && side == 0) {
+                if (p.place >= 0)
+                    part_lse[(size_t)p.place * kRows + r] = lv;
+                else
+                    lse[row] = lv * 0.69314718055994531f;
+            }
+            ++uc;
+        }
     } else if (warp < 8) {
-        // ----------------------------------------- softmax, Q, epilogue
+        // ----------------------------------------------------- softmax, Q
         // TMEM lane i holds pair i % 64 of this CTA's 64: keys of the tile's first
-        // block of 64 (and output columns 0..255) for i < 64, of the second (and
-        // columns 256..511) for the others; hs halves both once more.
+        // block of 64 for i < 64, of the second for the others; hs halves both
+        // once more.
         const int hs = warp >> 2;
         const int i = (warp & 3) * 32 + lane;
         const int side = i >> 6, lr = i & 63;
@@ -605,6 +770,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         const int grp = side * 2 + hs;
         float* red = reinterpret_cast<float*>(sgen + kOffRed);
         float* lsum_s = reinterpret_cast<float*>(sgen + kOffLsum);
+        float* max_s = reinterpret_cast<float*>(sgen + kOffMax);
         int* bad_s = reinterpret_cast<int*>(sgen + kOffBad);
         const uint32_t qt0 = mapa(bar(B_QT), 0), sfree0 = mapa(bar(B_SFREE), 0), pfull0 = mapa(bar(B_PFULL), 0);
         bool ok = true;
@@ -647,43 +813,36 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (lane == 0) mbar_arrive_cluster(qt0);
             return true;
         };
-        const int col0 = side * 256 + 128 * hs;             // output columns of this warp
-        // the next part with keys; units without any are written on the way
-        Walk walk(pc);
-        auto advance = [&](Part& p) -> bool {
-            while (walk.next(args, pc, p)) {
-                if (p.a < p.b) return true;
-                if (r < p.u.n * args.Hq) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)p.u.t * args.Hq + r) * kDv + col0);
-                    for (int v = 0; v < 16; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (grp == 0) lse[(size_t)p.u.t * args.Hq + r] = -INFINITY;
+        // the next part with keys, and what this thread's pair sees
+        int np = 0;
+        auto advance = [&](PartInfo& p, Visible& vis) -> bool {
+            do {
+                if (!take_part(np++, p)) {
+                    ok = false;
+                    return false;
                 }
-                __syncwarp();
+                if (p.nt < 0) return false;
+            } while (p.nt == 0);
+            vis.hi = -1;
+            vis.lo = vis.sink_end = 0;
+            if (r < p.rows) {
+                const int t = p.t + r / args.Hq;
+                Visible v;
+                if (row_sees(args, args.pg.seq[t], args.pos[t], v)) vis = v;
             }
-            return false;
+            return true;
         };
-        Part cur, nxt;
-        bool have = advance(cur);
+        PartInfo u, un;
+        Visible vis, vn;
+        bool have = advance(u, vis);
         if (have) ok = write_q(0);
         int g = 0, uc = 0;
         while (have && ok) {
-            const Unit& u = cur.u;
-            const int nt = cur.b - cur.a;
-            const bool live = r < u.n * args.Hq;
-            Visible vis;
-            vis.hi = -1;
-            vis.lo = vis.sink_end = 0;
-            if (live) {
-                long long base;
-                const int* bt;
-                const int t = u.t + r / args.Hq;
-                const int n = row_keys(args.pg, args.pos, nullptr, t, args.T, 0, &base, &bt);
-                if (n > 0) vis = visible_of(n, args.pos[t], args.window, args.sinks);
-            }
-            const bool more = advance(nxt);
+            const int nt = u.nt;
+            bool more = false;
             float m_use = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++g) {
-                const int key0 = u.key0(cur.a + j);
+                const int key0 = u.key0(j);
                 const bool whole = u.all_see(key0, kTile);
                 if (!wait_all(bar(B_SFULL), g & 1, abort_flag, 1300, g)) { ok = false; break; }
                 tc_fence_after();
@@ -754,7 +913,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                     for (int e = 0; e < w; ++e) ps[e] += ps[e + w];
                 l = l * f + ps[0];
                 // PV(g-1) has read P and written O
-                if (j > 0 && !wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1320, g)) { ok = false; break; }
+                if (g > 0 && !wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1320, g)) { ok = false; break; }
                 if (__any_sync(0xffffffffu, rescale)) {
                     tc_fence_after();
 #pragma unroll 1
@@ -803,74 +962,20 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(pfull0);
+                if (j == 0) more = advance(un, vn);     // while the tensor pipe is busy
             }
             ring += 2 + 4 * nt;
             rope += 1 + nt;
             if (!ok) break;
-            // every QK of this unit has completed: Q makes room for the next unit's
-            if (more && !write_q(uc + 1)) { ok = false; break; }
-            // row sum over the four threads of the row
+            // sum and maximum for the warps that take O
             lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
+            if (grp == 0) max_s[(uc & 1) * 64 + lr] = m_use;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_LSUM));
-            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g)) { ok = false; break; }
-            const float* ls = lsum_s + (uc & 1) * 256 + lr;
-            l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
-            if (!wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1350, g)) { ok = false; break; }
-            tc_fence_after();
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            const float lv = l != 0.f ? m_use + __log2f(l) : -INFINITY;
-            const bool split = cur.split();
-            const size_t prow = ((size_t)cid * 2 + (cur.start < pc.w0 ? 0 : 1)) * kRows + r;
-            float4* po = reinterpret_cast<float4*>(part_o) + (prow - r) * (kDv / 4) + r;
-            // rows leave through the shared memory of this warp's P, 64 bytes each at
-            // a time, so that stores cover whole sectors
-            const uint32_t stage = sbase + kOffP + side * kSlab;
-#pragma unroll 1
-            for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_addr + kColO + 128 * hs + q4 * 32, o);
-                tmem_wait_ld();
-                if (split) {
-                    if (live) {
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            po[(size_t)(col0 / 4 + q4 * 8 + v) * kRows] =
-                                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                               __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-                        st_shared_v4(stage + lr * 128 + (((4 * hs + v) ^ (lr & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) {
-                        const int row = (lr & 32) + it * 8 + (lane >> 2), v = lane & 3;
-                        const uint4 w = ld_shared_v4(stage + row * 128 + (((4 * hs + v) ^ (row & 7)) << 4));
-                        const int rr = (int)rank * 64 + row;
-                        if (rr < u.n * args.Hq)
-                            *reinterpret_cast<uint4*>(out + ((size_t)u.t * args.Hq + rr) * kDv + col0 + q4 * 32 + v * 8) = w;
-                    }
-                }
-                __syncwarp();
-            }
-            // O is read: the next unit's first PV overwrites it once this warp
-            // hands over its first P
-            tc_fence_before();
-            if (live && grp == 0) {
-                if (split)
-                    part_lse[prow] = lv;
-                else
-                    lse[(size_t)u.t * args.Hq + r] = lv * 0.69314718055994531f;
-            }
-            cur = nxt;
+            // every QK of this unit has completed: Q makes room for the next unit's
+            if (more && !write_q(uc + 1)) break;
+            u = un;
+            vis = vn;
             have = more;
             ++uc;
         }
@@ -889,15 +994,15 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
     cluster_sync();   // both CTAs' MMAs, remote arrivals and copies are over
     tc_fence_after();
     if (warp == 9) tmem_dealloc_pair(tmem, 512);
-    cluster_sync();
 }
 
 // Joins the parts of a split unit, in the order of the clusters:
 //   lse = log sum_z 2^lse_z,  out = sum_z 2^(lse_z - lse) o_z.
-// One CTA per (cluster that ended a split unit, 4 of its pairs); its CTAs for
-// clusters that ended none leave at once.
-constexpr int kJoinRows = 4;
-constexpr int kJoinThreads = 256;
+// One CTA per (cluster that ended a split unit, 8 of its pairs, 128 columns);
+// its CTAs for clusters that ended none leave at once.
+constexpr int kJoinRows = 8;
+constexpr int kJoinCols = 128;
+constexpr int kJoinThreads = kJoinRows * kJoinCols / 4;
 
 __global__ void __launch_bounds__(kJoinThreads)
 mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
@@ -906,13 +1011,14 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
 {
     __shared__ float wz[kMaxClusters][kJoinRows];
     __shared__ int where[kMaxClusters];
+    griddep_launch();
     griddep_wait();
     const SplitDesc d = desc[blockIdx.x];
     const int r0 = blockIdx.y * kJoinRows;
     if (d.n_rows <= r0) return;
     const int parts = d.c_last - d.c_first + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp < kJoinRows) {
+    {
         // a warp per row, lanes over the parts
         const int r = r0 + warp;
         float v[3], m = -INFINITY;
@@ -935,33 +1041,27 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
 #pragma unroll
         for (int i = 0; i < 3; ++i)
             if (lane + 32 * i < parts) wz[lane + 32 * i][warp] = v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
-        if (lane == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
+        if (lane == 0 && blockIdx.z == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
     }
     __syncthreads();
-    // 4 rows x 128 groups of four columns, two per thread
-    const int rr = threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
-    constexpr int kStep = kJoinThreads / kJoinRows;
+    // a thread per row and group of four columns
+    const int rr = threadIdx.x % kJoinRows, c4 = blockIdx.z * (kJoinCols / 4) + threadIdx.x / kJoinRows;
     if (r0 + rr >= d.n_rows) return;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)c4 * kRows + r0 + rr;
+#pragma unroll 8
     for (int z = 0; z < parts; ++z) {
         const float w = wz[z][rr];
-        const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)where[z] * kRows * (kDv / 4) + r0 + rr;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 v = p[(size_t)(c4 + i * kStep) * kRows];
-            acc[i].x = fmaf(w, v.x, acc[i].x);
-            acc[i].y = fmaf(w, v.y, acc[i].y);
-            acc[i].z = fmaf(w, v.z, acc[i].z);
-            acc[i].w = fmaf(w, v.w, acc[i].w);
-        }
+        const float4 v = p[(size_t)where[z] * kRows * (kDv / 4)];
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4 + i * kStep] =
-            make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
+    reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4] =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
-static_assert(kMaxClusters <= 96 && kDv / 4 == 2 * kJoinThreads / kJoinRows, "the join's lanes and threads");
+static_assert(kMaxClusters <= 96 && kJoinThreads == 32 * kJoinRows, "the join's lanes and warps");
 
 }  // namespace cache_attn
 }  // namespace dsa

@@ -71,6 +71,10 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // launched without the attribute.)
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream start its prologue (it waits for this one
+// in griddep_wait before it reads global memory).
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Candidate range of query row t: s = 0..n-1 at cache rows base + s. Rows that
 // would reach outside the cache (a caller error) are clipped to it, so no
 // kernel ever reads out of bounds.
