@@ -159,8 +159,8 @@ int dsa_sparse_mla_attn_paged(const void* q, const void* kv_pages, int num_pages
  * sequence may be any tokens of it, in any order; those of a chunk are
  * cheapest next to each other. Probabilities are rounded to bf16 for the
  * product with the values; logits, maxima and sums are fp32.
- * Supported: 1 <= Hq <= 128, d_qk = 576, d_v = 512, T * Hq < 2^31, sinks > 0
- * only with a window. workspace: dsa_mla_attn_paged_workspace_size(T, Hq)
+ * Supported: 1 <= Hq <= 128, d_qk = 576, d_v = 512, T * Hq < 2^31, S <= 2^30,
+ * T (S / 128 + 4) < 2^31, sinks > 0 only with a window. workspace: dsa_mla_attn_paged_workspace_size(T, Hq)
  * bytes; calls in flight at once, captured graphs among them, need one each.
  */
 size_t dsa_mla_attn_paged_workspace_size(int T, int Hq);

@@ -21,6 +21,7 @@ Entry points mirror the C ABI:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -406,10 +407,14 @@ def _cache_rows(q, kv_pages, page_size, block_table, seq, pos):
     return q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev
 
 
+@functools.lru_cache(maxsize=64)
+def _attn_ws_bytes(T: int, Hq: int) -> int:
+    return max(int(load_library().dsa_mla_attn_paged_workspace_size(T, Hq)), 256)
+
+
 def alloc_mla_attn_workspace(T: int, Hq: int, device=None) -> torch.Tensor:
     """Workspace of ``mla_attn_paged`` for T rows of Hq heads."""
-    n = int(load_library().dsa_mla_attn_paged_workspace_size(T, Hq))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_attn_ws_bytes(T, Hq), dtype=torch.uint8, device=device or "cuda")
 
 
 def alloc_mla_mass_workspace(n_seqs: int, device=None) -> torch.Tensor:
@@ -434,7 +439,7 @@ def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: fl
     lse = _new((T, Hq), torch.float32, dev, stream) if lse is None else \
         _arg(lse, "lse", torch.float32, (T, Hq), dev)
     if workspace is None:
-        workspace = _new(max(lib.dsa_mla_attn_paged_workspace_size(T, Hq), 256), torch.uint8, dev, stream)
+        workspace = _new(_attn_ws_bytes(T, Hq), torch.uint8, dev, stream)
     n_seqs, max_pages = block_table.shape
     _run(lib.dsa_mla_attn_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages, page_size,
          block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), T, Hq, d_qk, d_v, scale, window,

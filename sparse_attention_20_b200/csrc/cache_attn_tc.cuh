@@ -91,7 +91,7 @@ constexpr int kMinWork = 8;
 struct SplitDesc {
     int t, n_rows;          // first row, (row, head) pairs (0: nothing to join)
     int c_first, c_last;    // clusters that hold its parts
-    long long start, total; // its place on the line of work, the line's length
+    int start, total;       // its place on the line of work, the line's length
     int ncl, pad;
 };
 
@@ -182,123 +182,6 @@ __device__ __forceinline__ Unit unit_at(const Args& a, int t)
     return u;
 }
 
-// v / d, in 32 bits where they hold v (a 64-bit division takes some 150 clocks).
-__device__ __forceinline__ long long quotient(long long v, long long d)
-{
-    return ((v | d) >> 32) == 0 ? (long long)((uint32_t)v / (uint32_t)d) : v / d;
-}
-
-// This cluster's piece [w0, w1) of the line of work, and the unit it starts in.
-struct Piece {
-    long long w0, w1, total, first_start;
-    int first_t, ncl;
-    __device__ __forceinline__ int cluster_of(long long x) const { return (int)quotient((x + 1) * ncl - 1, total); }
-    __device__ __forceinline__ static long long begin(long long total, int ncl, int c) { return quotient(total * c, ncl); }
-};
-
-// Block-wide: finds the units' places on the line of work from seq and pos
-// (every CTA does so for itself; a row costs a thread a few loads).
-__device__ Piece plan(const Args& a, int cid, int clusters, uint8_t* smem)
-{
-    long long* s64 = reinterpret_cast<long long*>(smem);       // [16] warp sums, then the piece
-    int* s32 = reinterpret_cast<int*>(smem + 128);             // [16] last run start of each warp's rows
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = rows_per_unit(a.Hq);
-    const int per = ceil_div(a.T, kTcThreads);
-    const int r0 = min(a.T, tid * per), r1 = min(a.T, r0 + per);
-    auto breaks = [&](int t) { return t == 0 || a.pg.seq[t] != a.pg.seq[t - 1]; };
-    if (r0 < r1) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.pos + r0));
-    // start of the run that row r0 lies in: the last break before or at it
-    int last = -1;
-    for (int t = r0; t < r1; ++t)
-        if (breaks(t)) last = t;
-    int run = last;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run = max(run, y);
-    }
-    if (lane == 31) s32[warp] = run;
-    __syncthreads();
-    int before = __shfl_up_sync(0xffffffffu, run, 1);
-    if (lane == 0) before = -1;
-    for (int w = 0; w < warp; ++w) before = max(before, s32[w]);
-    // work of the units that start in this thread's rows
-    auto walk = [&](auto&& f) {
-        int start = before;
-        for (int t = r0; t < r1; ++t) {
-            if (breaks(t)) start = t;
-            if ((t - start) % G == 0) f(t, unit_at<1>(a, t).nt + kUnitCost);
-        }
-    };
-    long long sum = 0;
-    walk([&](int, int w) { sum += w; });
-    long long pre = sum;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += y;
-    }
-    if (lane == 31) s64[warp] = pre;
-    __syncthreads();
-    Piece p;
-    p.total = 0;
-    long long base = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-        if (w < warp) base += s64[w];
-        p.total += s64[w];
-    }
-    pre += base - sum;
-    p.ncl = (int)max(1ll, min((long long)clusters, p.total / kMinWork));
-    p.w0 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid) : p.total;
-    p.w1 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid + 1) : p.total;
-    __syncthreads();
-    if (p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum) {
-        long long at = pre;
-        bool found = false;
-        walk([&](int t, int w) {
-            if (!found && p.w0 < at + w) {
-                found = true;
-                s64[0] = at;
-                s32[0] = t;
-            }
-            at += w;
-        });
-    }
-    __syncthreads();
-    p.first_start = s64[0];
-    p.first_t = s32[0];
-    return p;
-}
-
-// A cluster's share of a unit: its tiles [a, b).
-struct Part {
-    Unit u;
-    long long start;
-    int a, b;
-    bool owns_empty;       // a unit without keys, to be written as zeros
-};
-
-// Walks the parts of a piece (a whole warp takes part).
-struct Walk {
-    long long at;
-    int t;
-    __device__ __forceinline__ Walk(const Piece& p) : at(p.first_start), t(p.first_t) {}
-    __device__ __forceinline__ bool next(const Args& a, const Piece& pc, Part& p)
-    {
-        while (at < pc.w1 && t < a.T && pc.w0 < pc.w1) {
-            p.u = unit_at<32>(a, t);
-            p.start = at;
-            const long long d = at + kUnitCost;
-            p.a = (int)max(0ll, min((long long)p.u.nt, pc.w0 - d));
-            p.b = (int)max(0ll, min((long long)p.u.nt, pc.w1 - d));
-            p.owns_empty = p.u.nt == 0 && at >= pc.w0;
-            at = d + p.u.nt;
-            t += p.u.n;
-            if (p.a < p.b || p.owns_empty) return true;
-        }
-        return false;
-    }
-};
-
 // A part as the other warps need it.
 struct PartInfo {
     int t, rows;               // first row, (row, head) pairs
@@ -317,6 +200,152 @@ struct PartInfo {
     }
 };
 static_assert(sizeof(PartInfo) == 64, "PartInfo");
+
+// This cluster's piece [w0, w1) of the line of work, and the unit it starts in.
+// (The host refuses a line of 2^31 or more; 64-bit divisions here cost a call
+// on 200 keys 1 us.)
+struct Piece {
+    int w0, w1, total, ncl;
+    int at, t, parts;       // where the walk goes on behind the first unit, parts handed out so far
+    // floor(total c / ncl)
+    __device__ __forceinline__ static int begin(int total, int ncl, int c)
+    {
+        const int q = total / ncl, r = total - q * ncl;
+        return c * q + c * r / ncl;
+    }
+    // the cluster whose piece holds place x
+    __device__ __forceinline__ int cluster_of(int x) const
+    {
+        int c = min(ncl - 1, x / max(1, total / ncl));
+        while (begin(total, ncl, c) > x) --c;
+        return c;
+    }
+};
+
+// The piece's share of unit u at place `at`, if any: written to *out, and
+// described for the join where the cluster ends a unit that others began.
+__device__ __forceinline__ bool part_of(const Args& a, const Piece& pc, int cid, const Unit& u, int at, PartInfo* out,
+                                        SplitDesc* desc)
+{
+    const int d = at + kUnitCost;
+    const int b0 = max(0, min(u.nt, pc.w0 - d)), b1 = max(0, min(u.nt, pc.w1 - d));
+    if (b0 >= b1 && (u.nt > 0 || at < pc.w0)) return false;
+    PartInfo i;
+    i.t = u.t;
+    i.rows = u.n * a.Hq;
+    i.hi = u.hi;
+    i.min_hi = u.min_hi;
+    i.max_lo = u.max_lo;
+    i.sink_end = u.sink_end;
+    i.ns = u.ns;
+    i.m0 = u.m0;
+    i.a = b0;
+    i.nt = b1 - b0;
+    i.place = b0 > 0 || b1 < u.nt ? cid * 2 + (at < pc.w0 ? 0 : 1) : -1;
+    i.pad = 0;
+    i.bt = u.bt;
+    i.pad2 = 0;
+    *out = i;
+    if (desc && b1 == u.nt && b0 > 0) {
+        SplitDesc s;
+        s.t = u.t;
+        s.n_rows = i.rows;
+        s.c_first = pc.cluster_of(d);
+        s.c_last = cid;
+        s.start = at;
+        s.total = pc.total;
+        s.ncl = pc.ncl;
+        s.pad = 0;
+        *desc = s;
+    }
+    return true;
+}
+
+// Block-wide: finds the units' places on the line of work from seq and pos
+// (every CTA does so for itself; a row costs a thread a few loads), and hands
+// out the part of the unit that this cluster's piece starts in.
+__device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo* first, SplitDesc* desc,
+                      uint32_t first_bar)
+{
+    int* sums = smem;                   // [16] warp sums
+    int* runs = smem + kPlanWarps;      // [16] last run start of each warp's rows
+    int* found = smem + 2 * kPlanWarps; // place and first row of the unit
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = rows_per_unit(a.Hq);
+    const int per = (a.T + kTcThreads - 1) / kTcThreads;
+    const int r0 = min(a.T, tid * per), r1 = min(a.T, r0 + per);
+    if (r0 < r1) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.pos + r0));
+    auto breaks = [&](int t) { return t == 0 || a.pg.seq[t] != a.pg.seq[t - 1]; };
+    // start of the run that row r0 lies in: the last break before or at it (a
+    // unit of one row starts anywhere)
+    int before = 0;
+    if (G > 1) {
+        int last = -1;
+        for (int t = r0; t < r1; ++t)
+            if (breaks(t)) last = t;
+        int run = last;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run = max(run, y);
+        }
+        if (lane == 31) runs[warp] = run;
+        __syncthreads();
+        before = __shfl_up_sync(0xffffffffu, run, 1);
+        if (lane == 0) before = -1;
+        for (int w = 0; w < warp; ++w) before = max(before, runs[w]);
+    }
+    // work of the units that start in this thread's rows
+    Unit u;
+    int sum = 0, start = before;
+    for (int t = r0; t < r1; ++t) {
+        if (G > 1 && breaks(t)) start = t;
+        if (G == 1 || (t - start) % G == 0) {
+            u = unit_at<1>(a, t);
+            sum += u.nt + kUnitCost;
+        }
+    }
+    int pre = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
+    }
+    if (lane == 31) sums[warp] = pre;
+    __syncthreads();        // also orders the descriptor's default before a part's
+    Piece p;
+    p.total = 0;
+    pre -= sum;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w < warp) pre += sums[w];
+        p.total += sums[w];
+    }
+    p.ncl = max(1, min(clusters, p.total / kMinWork));
+    p.w0 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid) : p.total;
+    p.w1 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid + 1) : p.total;
+    if (p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum) {
+        int at = pre;
+        if (per > 1) {
+            start = before;
+            for (int t = r0; t < r1; ++t) {
+                if (G > 1 && breaks(t)) start = t;
+                if (G == 1 || (t - start) % G == 0) {
+                    u = unit_at<1>(a, t);
+                    if (p.w0 < at + u.nt + kUnitCost) break;
+                    at += u.nt + kUnitCost;
+                }
+            }
+        }
+        found[0] = at + kUnitCost + u.nt;
+        found[1] = u.t + u.n;
+        found[2] = part_of(a, p, cid, u, at, first, desc) ? 1 : 0;
+        if (found[2]) mbar_arrive(first_bar);
+    }
+    __syncthreads();
+    p.at = found[0];
+    p.t = found[1];
+    p.parts = p.w0 < p.w1 ? found[2] : 0;
+    return p;
+}
 
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
 {
@@ -419,12 +448,13 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
     __syncthreads();
     cluster_arrive();     // the other CTA's barriers exist before any remote arrival
     griddep_wait();
-    const Piece pc = plan(args, cid, clusters, sgen + kOffPlan);
+    PartInfo* infos = reinterpret_cast<PartInfo*>(sgen + kOffParts);
+    if (rank == 0 && threadIdx.x == 0) desc[cid].n_rows = 0;
+    const Piece pc = plan(args, cid, clusters, reinterpret_cast<int*>(sgen + kOffPlan), infos,
+                          rank == 0 ? desc + cid : nullptr, bar(B_PART));
     cluster_wait();
     tc_fence_after();
     const uint32_t tmem = *taddr_slot;
-    bool issued_any = false;
-    PartInfo* infos = reinterpret_cast<PartInfo*>(sgen + kOffParts);
     // part n of the piece (false: given up); it is handed back at once
     auto take_part = [&](int n, PartInfo& p) -> bool {
         const int at = n % kAhead;
@@ -627,55 +657,39 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (rslot == 0) rph ^= 1u;
             for (int j = 0; j < p.nt && ok; ++j) {
                 ok = qk();
-                issued_any = true;
                 ++g;
                 if (ok && j > 0) ok = pv(g - 2, j == 1);
             }
             if (ok) ok = pv(g - 1, p.nt == 1);
             ++n_units;
         }
+        // the last signals of the other CTA
+        if (ok && n_units > 0)
+            wait_lanes(lane == 0 ? bar(B_SFREE) : bar(B_OFREE), lane == 0 ? (uint32_t)((g - 1) & 1) : (uint32_t)((n_units - 1) & 1),
+                       abort_flag, 1260, g);
     } else if (warp == 10) {
         // ------------------------------------------------------------ parts
-        if (rank == 0 && el) desc[cid].n_rows = 0;
-        Walk walk(pc);
-        Part p;
-        bool more = true;
-        for (int np = 0; more; ++np) {
-            const int at = np % kAhead;
-            more = walk.next(args, pc, p);
-            if (!wait_lanes(bar(B_PARTFREE + at), (uint32_t)(((np / kAhead) & 1) ^ 1), abort_flag, 1060, np)) break;
-            if (el) {
-                PartInfo i;
-                i.t = p.u.t;
-                i.rows = p.u.n * args.Hq;
-                i.hi = p.u.hi;
-                i.min_hi = p.u.min_hi;
-                i.max_lo = p.u.max_lo;
-                i.sink_end = p.u.sink_end;
-                i.ns = p.u.ns;
-                i.m0 = p.u.m0;
-                i.a = p.a;
-                i.nt = more ? p.b - p.a : -1;
-                i.place = p.a > 0 || p.b < p.u.nt ? cid * 2 + (p.start < pc.w0 ? 0 : 1) : -1;
-                i.pad = 0;
-                i.bt = p.u.bt;
-                i.pad2 = 0;
-                infos[at] = i;
-                mbar_arrive(bar(B_PART + at));
-                if (more && rank == 0 && p.b == p.u.nt && p.a > 0) {
-                    SplitDesc d;
-                    d.t = p.u.t;
-                    d.n_rows = p.u.n * args.Hq;
-                    d.c_first = pc.cluster_of(p.start + kUnitCost);
-                    d.c_last = cid;
-                    d.start = p.start;
-                    d.total = pc.total;
-                    d.ncl = pc.ncl;
-                    d.pad = 0;
-                    desc[cid] = d;
+        int at = pc.at, t = pc.t, np = pc.parts;
+        while (true) {
+            const bool more = pc.w0 < pc.w1 && at < pc.w1 && t < args.T;
+            const int slot = np % kAhead;
+            if (!wait_lanes(bar(B_PARTFREE + slot), (uint32_t)(((np / kAhead) & 1) ^ 1), abort_flag, 1060, np)) break;
+            if (!more) {
+                if (el) {
+                    infos[slot].nt = -1;
+                    mbar_arrive(bar(B_PART + slot));
                 }
+                break;
             }
-            __syncwarp();
+            const Unit u = unit_at<32>(args, t);
+            bool mine = false;
+            if (el) {
+                mine = part_of(args, pc, cid, u, at, infos + slot, rank == 0 ? desc + cid : nullptr);
+                if (mine) mbar_arrive(bar(B_PART + slot));
+            }
+            np += __any_sync(0xffffffffu, mine) ? 1 : 0;
+            at += kUnitCost + u.nt;
+            t += u.n;
         }
     } else if (warp >= 12) {
         // ---------------------------------------------------------- O out
@@ -715,10 +729,15 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             tc_fence_after();
             float4* po = reinterpret_cast<float4*>(part_o) + (size_t)max(p.place, 0) * kRows * (kDv / 4) + r;
 #pragma unroll 1
-            for (int c0 = 0; c0 < 256; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_addr + kColO + c0, o);
+            for (int h0 = 0; h0 < 256; h0 += 64) {
+                uint32_t o2[2][32];
+                tmem_ld32(tmem + lane_addr + kColO + h0, o2[0]);
+                tmem_ld32(tmem + lane_addr + kColO + h0 + 32, o2[1]);
                 tmem_wait_ld();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const uint32_t (&o)[32] = o2[hh];
+                    const int c0 = h0 + 32 * hh;
                 if (live && p.place >= 0) {
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
@@ -742,6 +761,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
+                }
                 }
                 __syncwarp();
             }
@@ -981,9 +1001,10 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         }
     }
 
-    if (warp == 9 && issued_any) {
-        // every MMA issued completes before TMEM is released
-        mma_commit_pair(bar(B_DRAIN), el);
+    if (warp == 9) {
+        // every MMA issued, and every signal to either CTA, completes before TMEM
+        // and shared memory are given up
+        if (rank == 0) mma_commit_pair(bar(B_DRAIN), el);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(bar(B_DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
@@ -991,7 +1012,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // both CTAs' MMAs, remote arrivals and copies are over
+    cluster_sync_relaxed();   // both CTAs' MMAs, remote arrivals and copies are over
     tc_fence_after();
     if (warp == 9) tmem_dealloc_pair(tmem, 512);
 }

@@ -1276,6 +1276,7 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     // the most work there can be bounds the clusters with a piece of it
     const long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
     const long long work = T * (tiles + kUnitCost);
+    if (work > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T=%d rows over a table of %lld keys", T, tiles * kTile);
     const int clusters = (int)std::max(1ll, std::min<long long>(work / kMinWork,
                                                                 std::min(kMaxClusters, std::max(1, num_sms() / 2))));
     launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1, tq4,
