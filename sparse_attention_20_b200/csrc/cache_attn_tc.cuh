@@ -66,7 +66,7 @@ constexpr int kOffBad = kOffMax + 2 * 64 * 4;         // [2][8] flags of the sof
 constexpr int kAhead = 4;                             // parts handed out ahead
 constexpr int kOffParts = kOffBad + 64;               // [kAhead] PartInfo
 constexpr int kOffPlan = kOffParts + kAhead * 64;
-constexpr int kTcSmem = kOffPlan + 256 + 1024;        // + alignment slack
+constexpr int kTcSmem = kOffPlan + 384 + 1024;        // + alignment slack
 static_assert(kTcSmem <= 232448, "shared memory");
 
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
@@ -86,6 +86,11 @@ constexpr int kMaxClusters = 74;
 constexpr int kUnitCost = 3;
 // Least work of a cluster: below it more clusters only add parts to join.
 constexpr int kMinWork = 8;
+// Where there are no more units than clusters and the largest is at most this
+// much above an even piece, each cluster takes a unit whole: parts written and
+// joined again cost more than the evenness gains (64 windows of 1024 keys: 48
+// us cut evenly, MEASURED whole).
+constexpr int kWholeSlack = 4;
 
 // A split unit that the cluster of its last tile describes for the join.
 struct SplitDesc {
@@ -269,7 +274,8 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
 {
     int* sums = smem;                   // [16] warp sums
     int* runs = smem + kPlanWarps;      // [16] last run start of each warp's rows
-    int* found = smem + 2 * kPlanWarps; // place and first row of the unit
+    int* found = smem + 2 * kPlanWarps; // where the walk goes on, parts handed out
+    int* units = smem + 3 * kPlanWarps; // [16] units that start in each warp's rows, and their largest
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = rows_per_unit(a.Hq);
     const int per = (a.T + kTcThreads - 1) / kTcThreads;
@@ -296,12 +302,24 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
     }
     // work of the units that start in this thread's rows
     Unit u;
-    int sum = 0, start = before;
+    int sum = 0, start = before, n_units = 0, largest = 0;
     for (int t = r0; t < r1; ++t) {
         if (G > 1 && breaks(t)) start = t;
         if (G == 1 || (t - start) % G == 0) {
             u = unit_at<1>(a, t);
             sum += u.nt + kUnitCost;
+            largest = max(largest, u.nt + kUnitCost);
+            ++n_units;
+        }
+    }
+    const int here = n_units;
+    if (per == 1) {
+        const unsigned m = __ballot_sync(0xffffffffu, here > 0);
+        n_units = __popc(m & ((1u << lane) - 1u));
+        largest = __reduce_max_sync(0xffffffffu, largest);
+        if (lane == 0) {
+            units[2 * warp] = __popc(m);
+            units[2 * warp + 1] = largest;
         }
     }
     int pre = sum;
@@ -322,7 +340,34 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
     p.ncl = max(1, min(clusters, p.total / kMinWork));
     p.w0 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid) : p.total;
     p.w1 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid + 1) : p.total;
-    if (p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum) {
+    bool mine = p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum;
+    if (per == 1) {
+        int all = 0;
+        largest = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) {
+            if (w < warp) n_units += units[2 * w];
+            all += units[2 * w];
+            largest = max(largest, units[2 * w + 1]);
+        }
+        if (all <= p.ncl && largest <= p.total / p.ncl + kWholeSlack) {
+            // unit cid, whole; its thread alone knows where it lies
+            mine = here > 0 && n_units == cid;
+            p.w0 = 0;
+            p.w1 = cid < all ? p.total : 0;
+            if (mine) {
+                p.w0 = pre;
+                p.w1 = pre + sum;
+            }
+            p.t = -1;
+        } else {
+            p.t = 0;
+        }
+    } else {
+        p.t = 0;
+    }
+    const bool whole = p.t < 0;
+    if (mine) {
         int at = pre;
         if (per > 1) {
             start = before;
@@ -341,9 +386,9 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
         if (found[2]) mbar_arrive(first_bar);
     }
     __syncthreads();
-    p.at = found[0];
-    p.t = found[1];
     p.parts = p.w0 < p.w1 ? found[2] : 0;
+    p.at = whole ? p.w1 : found[0];     // a whole unit is all of its cluster's work
+    p.t = found[1];
     return p;
 }
 
@@ -1019,68 +1064,92 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
 
 // Joins the parts of a split unit, in the order of the clusters:
 //   lse = log sum_z 2^lse_z,  out = sum_z 2^(lse_z - lse) o_z.
-// One CTA per (cluster that ended a split unit, 8 of its pairs, 128 columns);
-// its CTAs for clusters that ended none leave at once.
+// CTAs take items of 8 pairs x 256 columns of the units that the clusters'
+// descriptors name.
 constexpr int kJoinRows = 8;
-constexpr int kJoinCols = 128;
-constexpr int kJoinThreads = kJoinRows * kJoinCols / 4;
+constexpr int kJoinCols = 256;
+constexpr int kJoinThreads = kJoinRows * kJoinCols / 8;       // two groups of four columns a thread
+constexpr int kJoinItems = kRows / kJoinRows * (kDv / kJoinCols);   // of a full unit
 
 __global__ void __launch_bounds__(kJoinThreads)
 mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                           const SplitDesc* __restrict__ desc, int Hq, __nv_bfloat16* __restrict__ out,
+                           const SplitDesc* __restrict__ desc, int clusters, int Hq, __nv_bfloat16* __restrict__ out,
                            float* __restrict__ lse)
 {
     __shared__ float wz[kMaxClusters][kJoinRows];
     __shared__ int where[kMaxClusters];
+    __shared__ int active[kMaxClusters];       // clusters that ended a split unit
+    __shared__ int n_active;
     griddep_launch();
     griddep_wait();
-    const SplitDesc d = desc[blockIdx.x];
-    const int r0 = blockIdx.y * kJoinRows;
-    if (d.n_rows <= r0) return;
-    const int parts = d.c_last - d.c_first + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    {
-        // a warp per row, lanes over the parts
-        const int r = r0 + warp;
-        float v[3], m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int z = lane + 32 * i;
-            v[i] = -INFINITY;
-            if (z >= parts) continue;
-            const int c = d.c_first + z;
-            const int at = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
-            if (warp == 0) where[z] = at;
-            if (r < d.n_rows) v[i] = part_lse[at * kRows + r];
-            m = fmaxf(m, v[i]);
+    if (warp == 0) {
+        int n = 0;
+        for (int c0 = 0; c0 < clusters; c0 += 32) {
+            const bool is = c0 + lane < clusters && desc[c0 + lane].n_rows > 0;
+            const unsigned m = __ballot_sync(0xffffffffu, is);
+            if (is) active[n + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
+            n += __popc(m);
         }
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ms = m == -INFINITY ? 0.f : m;
-        float l = (exp2f(v[0] - ms) + exp2f(v[1] - ms)) + exp2f(v[2] - ms);
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const float total = l != 0.f ? ms + log2f(l) : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (lane + 32 * i < parts) wz[lane + 32 * i][warp] = v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
-        if (lane == 0 && blockIdx.z == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
+        if (lane == 0) n_active = n;
     }
     __syncthreads();
-    // a thread per row and group of four columns
-    const int rr = threadIdx.x % kJoinRows, c4 = blockIdx.z * (kJoinCols / 4) + threadIdx.x / kJoinRows;
-    if (r0 + rr >= d.n_rows) return;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)c4 * kRows + r0 + rr;
-#pragma unroll 8
-    for (int z = 0; z < parts; ++z) {
-        const float w = wz[z][rr];
-        const float4 v = p[(size_t)where[z] * kRows * (kDv / 4)];
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    for (int item = blockIdx.x; item < n_active * kJoinItems; item += gridDim.x) {
+        const SplitDesc d = desc[active[item / kJoinItems]];
+        const int e = item % kJoinItems, r0 = e / (kDv / kJoinCols) * kJoinRows, z4 = e % (kDv / kJoinCols);
+        if (d.n_rows <= r0) continue;
+        const int parts = d.c_last - d.c_first + 1;
+        {
+            // a warp per row, lanes over the parts
+            const int r = r0 + warp;
+            float v[3], m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int z = lane + 32 * i;
+                v[i] = -INFINITY;
+                if (z >= parts) continue;
+                const int c = d.c_first + z;
+                const int at = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
+                if (warp == 0) where[z] = at;
+                if (r < d.n_rows) v[i] = part_lse[at * kRows + r];
+                m = fmaxf(m, v[i]);
+            }
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float ms = m == -INFINITY ? 0.f : m;
+            float l = (exp2f(v[0] - ms) + exp2f(v[1] - ms)) + exp2f(v[2] - ms);
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const float total = l != 0.f ? ms + log2f(l) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (lane + 32 * i < parts) wz[lane + 32 * i][warp] = v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
+            if (lane == 0 && z4 == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
+        }
+        __syncthreads();
+        const int rr = threadIdx.x % kJoinRows, c4 = z4 * (kJoinCols / 4) + threadIdx.x / kJoinRows;
+        constexpr int kStep = kJoinThreads / kJoinRows;
+        if (r0 + rr < d.n_rows) {
+            float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+            const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)c4 * kRows + r0 + rr;
+#pragma unroll 4
+            for (int z = 0; z < parts; ++z) {
+                const float w = wz[z][rr];
+                const float4* pz = p + (size_t)where[z] * kRows * (kDv / 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 v = __ldcs(pz + (size_t)i * kStep * kRows);
+                    acc[i].x = fmaf(w, v.x, acc[i].x);
+                    acc[i].y = fmaf(w, v.y, acc[i].y);
+                    acc[i].z = fmaf(w, v.z, acc[i].z);
+                    acc[i].w = fmaf(w, v.w, acc[i].w);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4 + i * kStep] =
+                    make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
+        }
+        __syncthreads();      // the weights make room for the next item's
     }
-    reinterpret_cast<uint2*>(out + ((size_t)d.t * Hq + r0 + rr) * kDv)[c4] =
-        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 static_assert(kMaxClusters <= 96 && kJoinThreads == 32 * kJoinRows, "the join's lanes and warps");
 

@@ -1284,8 +1284,9 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
                reinterpret_cast<__nv_bfloat16*>(out), lse, part_o, part_lse, desc);
     DSA_LAUNCH_CHECK("mla_attn_paged_tc_kernel");
     if (clusters > 1) {
-        launch_pdl(mla_attn_paged_join_kernel, dim3(clusters, kRows / kJoinRows, kDv / kJoinCols),
-                   dim3(kJoinThreads), 0, st, part_o, part_lse, desc, Hq, reinterpret_cast<__nv_bfloat16*>(out), lse);
+        launch_pdl(mla_attn_paged_join_kernel, dim3(std::min(clusters * kJoinItems, 8 * num_sms())),
+                   dim3(kJoinThreads), 0, st, part_o, part_lse, desc, clusters, Hq,
+                   reinterpret_cast<__nv_bfloat16*>(out), lse);
         DSA_LAUNCH_CHECK("mla_attn_paged_join_kernel");
     }
     return DSA_OK;
