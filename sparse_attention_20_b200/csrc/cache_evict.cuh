@@ -1,6 +1,8 @@
 // Eviction from the paged caches by accumulated attention weight: which
 // positions of each sequence stay, and the move of their rows to the front.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -262,10 +264,50 @@ cache_evict_select_kernel(const float* __restrict__ mass, long long ld, const in
 // -------------------------------------------------------------- compaction
 
 constexpr int kMoveThreads = 512;
-constexpr int kMoveBuf = 40 * 1024;                  // bytes of a block of rows in a CTA, of two
-constexpr int kMoveRows = kMoveBuf / 64;             // most rows of a block
-constexpr int kMoveSmem = 2 * kMoveBuf + 3 * kMoveRows * 8;   // two CTAs a SM
 constexpr int kMassPer = 16;
+
+// How a compaction is laid out: the width of a slice of columns, the CTAs of a
+// cluster, bytes and most rows of a block in a CTA (two are in turn).
+struct MoveShape {
+    int slice, size, buf, rows;
+    size_t smem() const { return 2 * (size_t)buf + 3 * (size_t)rows * 8; }
+};
+
+// All CTAs should run at once (352 CTAs on 296 places took 80 us for what 256
+// take MEASURED), with 7.5 MB in flight to fill HBM, and in few blocks, each of
+// which costs some 2.5 us of latency: one sequence's 16384 rows in two blocks of
+// 96 KB per CTA, one CTA a SM; 32 sequences' 4099 rows in 40 KB, two CTAs a SM.
+inline MoveShape move_shape(int n_seqs, int kv_bytes, int k_bytes, bool mass, int keep, int sms)
+{
+    static const int cuts[] = {1, 2, 3, 4, 6, 9, 12, 18};
+    MoveShape best = {128, 1, 40 * 1024, 640};
+    double best_us = 1e30;
+    long long best_total = 0;
+    for (int resident = 1; resident <= 2; ++resident)
+        for (int n : cuts)
+            for (int size = 1; size <= 8; size *= 2) {
+                MoveShape m;
+                m.slice = ((kv_bytes + n - 1) / n + 31) / 32 * 32;
+                m.size = size;
+                m.buf = resident == 1 ? 96 * 1024 : 40 * 1024;
+                m.rows = resident == 1 ? 1024 : 640;
+                if (m.slice < 64 && n > 1) continue;
+                const long long total = (long long)n_seqs * size *
+                                        (ceil_div(kv_bytes, m.slice) + ceil_div(k_bytes, m.slice) + (mass ? 1 : 0));
+                // clusters of 4 and 8 do not fill every group of SMs
+                if (total > (long long)resident * (size == 8 ? sms * 13 / 15 : size == 4 ? sms * 14 / 15 : sms)) continue;
+                const int rows = std::min(m.rows, m.buf / m.slice);
+                const double blocks = ((double)keep / size + rows - 1) / rows;
+                const double bytes = 2.0 * n_seqs * keep * (kv_bytes + k_bytes + 4);
+                const double us = std::max(2.5 * blocks, bytes / 6e6 / std::min(1.0, total * m.buf / 7.5e6));
+                if (us < best_us * 0.99 || (us < best_us * 1.01 && total > best_total)) {
+                    best_us = us;
+                    best = m;
+                    best_total = total;
+                }
+            }
+    return best;
+}
 
 // Rows moved in place: row idx[j] of the sequence to row j, j < new_len, as
 // idx ascends and idx[j] >= j. A row may be written once all rows up to it are
@@ -281,11 +323,12 @@ struct MoveRows {
 };
 
 __global__ void __launch_bounds__(kMoveThreads)
-cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__ mass, int slice, const PagedRows pg,
-                     const int* __restrict__ keep_idx, int keep, const int* __restrict__ new_len)
+cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__ mass, const MoveShape shape,
+                     const PagedRows pg, const int* __restrict__ keep_idx, int keep, const int* __restrict__ new_len)
 {
     extern __shared__ __align__(16) uint8_t buf[];
-    int2* from_to = reinterpret_cast<int2*>(buf + 2 * kMoveBuf);   // [3][kMoveRows] pool rows, x < 0: stays
+    const int slice = shape.slice, max_rows = shape.rows;
+    int2* from_to = reinterpret_cast<int2*>(buf + 2 * shape.buf);  // [3][max_rows] pool rows, x < 0: stays
     const int rank = (int)cluster_ctarank(), size = (int)cluster_size();
     const int b = (int)(blockIdx.x / size), tid = threadIdx.x;
     const int S = pg.max_pages * pg.page_size;
@@ -320,7 +363,7 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     const MoveRows mv = y < kv.slices ? kv : keys;
     if (y >= kv.slices) y -= kv.slices;
     const int col = y * slice, width = min(slice, mv.bytes - col), pieces = width / 16;
-    const int rows = min(kMoveRows, kMoveBuf / width);             // of a block, in one CTA
+    const int rows = min(max_rows, shape.buf / width);             // of a block, in one CTA
     const int* bt = pg.block_table + (size_t)b * pg.max_pages;
     auto pool_row = [&](int s) -> int {
         const int page = bt[s / pg.page_size];
@@ -331,7 +374,7 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     const int blocks = (m + per - 1) / per;
     // where block k's rows of this CTA come from and go
     auto look_up = [&](int k) {
-        int2* ft = from_to + (k % 3) * kMoveRows;
+        int2* ft = from_to + (k % 3) * max_rows;
         for (int r = tid; r < rows; r += kMoveThreads) {
             const int j = (k * size + rank) * rows + r;
             int2 f = make_int2(-1, -1);
@@ -346,8 +389,8 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     // this thread's piece of every step-th row
     const int step = kMoveThreads / pieces, r_first = tid / pieces, p = tid - r_first * pieces;
     auto read = [&](int k) {
-        const int2* ft = from_to + (k % 3) * kMoveRows;
-        const uint32_t dst = smem_u32(buf) + (uint32_t)(k & 1) * kMoveBuf + p * 16;
+        const int2* ft = from_to + (k % 3) * max_rows;
+        const uint32_t dst = smem_u32(buf) + (uint32_t)(k & 1) * (uint32_t)shape.buf + p * 16;
         if (r_first < step)
             for (int r = r_first; r < rows; r += step)
                 if (ft[r].x >= 0)
@@ -358,12 +401,15 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     if (blocks > 0) read(0);
     if (blocks > 1) look_up(1);
     for (int k = 0; k < blocks; ++k) {
+        // block k is read everywhere: its copies have landed, so the barrier need
+        // not order anything (a release waits for the last block's stores)
         sm100::cp_async_wait_all();
-        cluster_sync();                // block k is read everywhere
+        __syncthreads();
+        if (size > 1) sm100::cluster_sync_relaxed();
         if (k + 1 < blocks) read(k + 1);
         if (k + 2 < blocks) look_up(k + 2);
-        const int2* ft = from_to + (k % 3) * kMoveRows;
-        const uint8_t* src = buf + (k & 1) * kMoveBuf + p * 16;
+        const int2* ft = from_to + (k % 3) * max_rows;
+        const uint8_t* src = buf + (k & 1) * shape.buf + p * 16;
         if (r_first < step)
             for (int r = r_first; r < rows; r += step)
                 if (ft[r].x >= 0)

@@ -1385,25 +1385,22 @@ int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int
                     kv_row_bytes, k_row_bytes, kMaxRowBytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dsa::PagedRows pg = paged_rows(block_table, nullptr, n_seqs, max_pages, page_size, num_pages);
-    // Narrow slices and clusters of up to 8 CTAs where there are few sequences,
-    // so that the whole card takes part.
-    const int sms = num_sms();
-    const int slice = (long long)n_seqs * dsa::ceil_div(kv_row_bytes, 128) >= sms ? 128 : 64;
+    const MoveShape shape = move_shape(n_seqs, kv_row_bytes, k_pages ? k_row_bytes : 0, mass != nullptr, keep,
+                                       num_sms());
     MoveRows kv, keys;
     kv.rows = reinterpret_cast<uint8_t*>(kv_pages);
     kv.bytes = kv_row_bytes;
-    kv.slices = dsa::ceil_div(kv_row_bytes, slice);
+    kv.slices = dsa::ceil_div(kv_row_bytes, shape.slice);
     keys.rows = reinterpret_cast<uint8_t*>(k_pages);
     keys.bytes = k_pages ? k_row_bytes : 0;
-    keys.slices = k_pages ? dsa::ceil_div(k_row_bytes, slice) : 0;
-    const int slices = kv.slices + keys.slices + (mass ? 1 : 0);
-    int size = 1;
-    while (size < 8 && (long long)n_seqs * slices * size < 2 * sms) size *= 2;
-    if ((long long)n_seqs * size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
-    cudaError_t e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+    keys.slices = k_pages ? dsa::ceil_div(k_row_bytes, shape.slice) : 0;
+    if ((long long)n_seqs * shape.size > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "n_seqs=%d", n_seqs);
+    cudaError_t e = cudaFuncSetAttribute(cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)shape.smem());
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cache_compact_kernel)");
-    e = launch_cluster(cache_compact_kernel, dim3(n_seqs * size, slices), dim3(kMoveThreads), kMoveSmem, size, st, kv,
-                       keys, mass, slice, pg, keep_idx, keep, new_len);
+    e = launch_cluster(cache_compact_kernel, dim3(n_seqs * shape.size, kv.slices + keys.slices + (mass ? 1 : 0)),
+                       dim3(kMoveThreads), shape.smem(), shape.size, st, kv, keys, mass, shape, pg, keep_idx, keep,
+                       new_len);
     if (e != cudaSuccess) return cuda_fail(e, "cache_compact_kernel");
     DSA_LAUNCH_CHECK("cache_compact_kernel");
     return DSA_OK;
