@@ -198,7 +198,7 @@ int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, 
  *   seq_len   int32 [n_seqs]
  *   keep_idx  int32 [n_seqs, keep] (out)  the positions, ascending, then -1
  *   new_len   int32 [n_seqs] (out)        min(n, keep)
- * Supported: keep >= 1, sinks + recent <= keep, max_len <= 2^30. No
+ * Supported: keep >= 1, sinks + recent <= keep, max_len and keep <= 2^30. No
  * workspace. Asynchronous on `stream`.
  */
 int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_len, int n_seqs, int keep, int sinks,

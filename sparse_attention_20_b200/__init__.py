@@ -382,6 +382,13 @@ def _run(fn, device, stream, *args) -> None:
         raise DSAError(rc, last_error())
 
 
+def _ints(**values) -> None:
+    """Sizes that a C int has to hold (ctypes would cut them silently)."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def _pages(t, name, cols=None, dtype=None, page_size=0, device=None):
     """Checked page pool [num_pages * page_size, cols]: (tensor, num_pages)."""
     t = _dev(t, name, device)
@@ -433,6 +440,7 @@ def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: fl
     Buffers not given are allocated on the stream that the call runs on."""
     q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
                                                                                   block_table, seq, pos)
+    _ints(window=window, sinks=sinks, page_size=page_size)
     lib = load_library()
     out = _new((T, Hq, d_v), torch.bfloat16, dev, stream) if out is None else \
         _arg(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
@@ -457,6 +465,7 @@ def mla_attn_mass_paged(q, kv_pages, page_size: int, block_table, seq, pos, lse,
     ``alloc_mla_mass_workspace``."""
     q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
                                                                                   block_table, seq, pos)
+    _ints(window=window, sinks=sinks, page_size=page_size)
     _arg(lse, "lse", torch.float32, (T, Hq), dev)
     n_seqs, max_pages = block_table.shape
     shape = (n_seqs, max_pages * page_size)
@@ -485,6 +494,7 @@ def cache_evict_select(mass, seq_len, keep: int, sinks: int = 0, recent: int = 0
     _arg(seq_len, "seq_len", torch.int32, (n_seqs,), dev)
     if keep <= 0:
         raise ValueError(f"keep = {keep} must be positive")
+    _ints(keep=keep, sinks=sinks, recent=recent, max_len=max_len)
     keep_idx = _new((n_seqs, keep), torch.int32, dev, stream) if keep_idx is None else \
         _arg(keep_idx, "keep_idx", torch.int32, (n_seqs, keep), dev)
     new_len = _new(n_seqs, torch.int32, dev, stream) if new_len is None else \

@@ -1259,6 +1259,10 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     if (need && (!workspace || ws_bytes < need || !al16(workspace)))
         return fail(DSA_ERR_WORKSPACE, "paged attention needs %zu workspace bytes (got %zu)", need, ws_bytes);
     const dsa::PagedRows pg = paged_rows(block_table, seq, n_seqs, max_pages, page_size, num_pages);
+    // the most work there can be bounds the clusters with a piece of it
+    const long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
+    const long long work = T * (tiles + kUnitCost);
+    if (work > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T=%d rows over a table of %lld keys", T, tiles * kTile);
     CUtensorMap tm4, tm1, tq4, tq1;
     const uint64_t pool_rows = (uint64_t)num_pages * page_size;
     if (int rc = make_tmap_slabs(&tm4, kv_pages, kDqk / 64, pool_rows, 4)) return rc;
@@ -1273,10 +1277,6 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     float* part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kPartBytes);
     SplitDesc* desc = reinterpret_cast<SplitDesc*>(reinterpret_cast<char*>(workspace) + kPartBytes + kPartLseBytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // the most work there can be bounds the clusters with a piece of it
-    const long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
-    const long long work = T * (tiles + kUnitCost);
-    if (work > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T=%d rows over a table of %lld keys", T, tiles * kTile);
     const int clusters = (int)std::max(1ll, std::min<long long>(work / kMinWork,
                                                                 std::min(kMaxClusters, std::max(1, num_sms() / 2))));
     launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1, tq4,
@@ -1345,7 +1345,8 @@ int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_le
     if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
         return fail(DSA_ERR_ARG, "sinks=%d and recent=%d must be >= 0 and at most keep=%d together", sinks, recent,
                     keep);
-    if (max_len > kMaxLen) return fail(DSA_ERR_UNSUPPORTED, "max_len=%d (supported: up to %d)", max_len, kMaxLen);
+    if (max_len > kMaxLen || keep > kMaxLen)
+        return fail(DSA_ERR_UNSUPPORTED, "max_len=%d, keep=%d (supported: up to %d)", max_len, keep, kMaxLen);
     // the smallest cluster with at most kSelShare positions a CTA, more CTAs where
     // there are few sequences, at most 8
     int size = 1;

@@ -26,11 +26,12 @@ BAD_ROWS = [(dict(q=None), -1), (dict(kv=None), -1), (dict(bt=None), -1), (dict(
             (dict(lse=None), -1), (dict(q=ODD), -1), (dict(kv=ODD), -1), (dict(lse=ODD), -1), (dict(T=0), -1),
             (dict(n_seqs=0), -1), (dict(max_pages=0), -1), (dict(num_pages=0), -1), (dict(page_size=32), -2),
             (dict(page_size=0), -2), (dict(num_pages=1 << 26), -2), (dict(Hq=0), -2), (dict(Hq=129), -2),
-            (dict(T=1 << 25), -2), (dict(d_qk=512), -2), (dict(window=-1), -1), (dict(sinks=-1), -1),
+            (dict(T=1 << 25), -2), (dict(max_pages=1 << 25), -2), (dict(d_qk=512), -2), (dict(window=-1), -1), (dict(sinks=-1), -1),
             (dict(sinks=4), -1)]
 
 
-@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(out=None), -1), (dict(out=ODD), -1), (dict(d_v=576), -2)])
+@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(out=None), -1), (dict(out=ODD), -1), (dict(d_v=576), -2),
+                                                    (dict(T=1 << 20, Hq=1, max_pages=1 << 24), -2)])
 def test_attention_refuses(lib, change, code):
     a = {**ATTN, **change}
     before = dsa.launch_count()
@@ -41,7 +42,7 @@ def test_attention_refuses(lib, change, code):
     assert rc == code and lib.dsa_last_error() and dsa.launch_count() == before
 
 
-@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(mass=None), -1), (dict(mass=ODD), -1), (dict(max_pages=1 << 25), -2),
+@pytest.mark.parametrize("change,code", BAD_ROWS + [(dict(mass=None), -1), (dict(mass=ODD), -1),
                                                     (dict(ws=None), -5), (dict(ws=ODD), -5), (dict(ws_bytes=64), -5)])
 def test_weights_refuse(lib, change, code):
     a = {**ATTN, "mass": FAKE, **change}
@@ -56,7 +57,7 @@ def test_weights_refuse(lib, change, code):
     (dict(mass=None), -1), (dict(seq_len=None), -1), (dict(idx=None), -1), (dict(new_len=None), -1),
     (dict(mass=ODD), -1), (dict(n_seqs=0), -1), (dict(max_len=0), -1), (dict(keep=0), -1), (dict(sinks=-1), -1),
     (dict(recent=-1), -1), (dict(sinks=60, recent=41), -1), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), -1),
-    (dict(max_len=(1 << 30) + 1), -2)])
+    (dict(max_len=(1 << 30) + 1), -2), (dict(keep=(1 << 30) + 1), -2)])
 def test_select_refuses(lib, change, code):
     a = {**dict(mass=FAKE, max_len=1000, seq_len=FAKE, n_seqs=2, keep=100, sinks=4, recent=8, idx=FAKE,
                 new_len=FAKE), **change}

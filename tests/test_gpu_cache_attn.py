@@ -49,6 +49,10 @@ CASES = [
     ([500, 200], [8, 8], 32, 64, 128, 128),
     ([500, 200], [3, 3], 128, 64, 4000, 16),     # window longer than the cache
     ([400], [3], 128, 64, 64, 1000),             # more first tokens than the cache holds
+    ([1], [1], 1, 64, 0, 0),                     # a query of one row in all
+    ([260, 129], [2, 3], 100, 64, 0, 0),         # 28 of a unit's 128 places unused
+    ([700], [5], 127, 192, 90, 2),
+    ([400, 300], [50, 45], 3, 64, 0, 0),         # 42 rows a unit, the runs' ends inside units
 ]
 
 
@@ -73,6 +77,71 @@ def test_many_rows_of_unequal_length():
     x = ref.make(lens, [1] * 180, 128, seed=5)
     out, lse = _attn(x)
     ref.check_attention(x, out, lse)
+
+
+def test_more_rows_than_the_plan_has_threads():
+    """Units of one row and of eight; runs that end anywhere; padding in between."""
+    lens = [20 + (37 * i) % 300 for i in range(100)]
+    x = ref.make(lens, [1 + i % 13 for i in range(100)], 128, seed=50)
+    x.seq[::17] = -1
+    assert x.q.shape[0] > 512
+    out, lse = _attn(x)
+    ref.check_attention(x, out, lse)
+    y = ref.make([900, 500, 40], [700, 333, 40], 16, seed=51)
+    out, lse = _attn(y, window=200, sinks=5)
+    ref.check_attention(y, out, lse, window=200, sinks=5)
+
+
+@pytest.mark.parametrize("lens", [[1000] * 40, [1000] * 39 + [1500], [1000] * 39 + [6000], [64] * 74, [64] * 75])
+def test_units_whole_or_cut(lens):
+    """As many even units as clusters, one longer than the others, and one more."""
+    x = ref.make(lens, [1] * len(lens), 128, seed=52)
+    out, lse = _attn(x)
+    ref.check_attention(x, out, lse)
+
+
+def test_outputs_on_any_16_byte_boundary():
+    x = ref.make([500], [3], 128, seed=53)
+    buf = torch.empty(3 * 128 * D_V + 8, dtype=torch.bfloat16, device="cuda")
+    at = 8 if (buf.data_ptr() % 32) == 0 else 0
+    out = buf[at:at + 3 * 128 * D_V].view(3, 128, D_V)
+    assert out.data_ptr() % 32 == 16
+    got = _attn(x, out=out)
+    ref.check_attention(x, *got)
+
+
+def test_workspace_may_hold_anything():
+    x = ref.make([9000, 7000], [1, 1], 128, seed=54)
+    ws = dsa.alloc_mla_attn_workspace(2, 128)
+    want = _attn(x)
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        got = _attn(x, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_one_stream_after_another_kernel_of_the_library():
+    """Calls back to back on one stream, each reading what the one before wrote:
+    the next call's positions, then its queries from this call's output."""
+    x = ref.make([3000, 2000], [1, 1], 128, seed=55)
+    ws, mws = dsa.alloc_mla_attn_workspace(2, 128), dsa.alloc_mla_mass_workspace(2)
+    outs, masses = [], []
+    mass = torch.zeros(2, x.S, device="cuda")
+    for i in range(6):
+        out, lse = dsa.mla_attn_paged(*x.args(), SCALE, D_V, workspace=ws)
+        dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, mass=mass, workspace=mws)
+        outs.append((out, lse, x.q.clone(), x.pos.clone()))
+        masses.append(mass.clone())
+        x.q[:, :, :D_V] = out
+        x.pos -= 7
+    torch.cuda.synchronize()
+    start = torch.zeros_like(mass)
+    for (out, lse, q, pos), m in zip(outs, masses):
+        x.q, x.pos = q, pos
+        ref.check_attention(x, out, lse)
+        want, tol = ref.received(x, lse, start)
+        assert bool(((m.double() - want).abs() <= tol + 2.0 ** -23 * want).all())
+        start = m
 
 
 def test_rows_without_keys_and_rows_beyond_the_table():
@@ -211,6 +280,33 @@ def test_another_stream_without_buffers_of_ones_own():
         ref.check_attention(x, *o)
 
 
+def test_binding_refuses():
+    x = ref.make([200], [2], 128, seed=56)
+    for kw in (dict(window=2 ** 32 + 5), dict(window=8, sinks=2 ** 40)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dsa.mla_attn_paged(*x.args(), SCALE, D_V, **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        dsa.mla_attn_paged(x.q.transpose(0, 1).contiguous().transpose(0, 1), *x.args()[1:], SCALE, D_V)
+    with pytest.raises(TypeError, match="bfloat16"):
+        dsa.mla_attn_paged(x.q.half(), *x.args()[1:], SCALE, D_V)
+    with pytest.raises(ValueError, match="whole number"):
+        dsa.mla_attn_paged(x.q, x.pages[:-1].contiguous(), *x.args()[2:], SCALE, D_V)
+    with pytest.raises(ValueError, match="shape"):
+        dsa.mla_attn_paged(*x.args()[:4], x.seq[:1].contiguous(), x.pos, SCALE, D_V)
+    with pytest.raises(ValueError, match="shape"):
+        dsa.mla_attn_paged(*x.args(), SCALE, D_V, out=torch.empty(2, 64, D_V, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(dsa.DSAError, match="workspace"):
+        dsa.mla_attn_paged(*x.args(), SCALE, D_V, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(dsa.DSAError, match="window"):
+        dsa.mla_attn_paged(*x.args(), SCALE, D_V, sinks=4)
+    lse = torch.zeros(2, 128, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, mass=torch.zeros(1, 8, device="cuda"))
+    with pytest.raises(ValueError, match="32 bits"):
+        dsa.cache_evict_select(torch.zeros(1, 64, device="cuda"), x.seq[:1].contiguous(), 8, recent=2 ** 31)
+    assert dsa.device_status() == 0
+
+
 def test_pool_offsets_beyond_32_bits():
     """A pool of 2^31 + elements: the sequence's pages lie at its end."""
     page = 256
@@ -279,6 +375,35 @@ def test_weights_of_each_row_and_head_sum_to_one():
     total = mass.double().sum(1).cpu()
     # a row's 128 heads give 128: each weight is within 1e-4 relative (ref.received's bound at these sizes)
     assert abs(total[0] - 12 * 128) <= 12 * 128 * 1e-4 and abs(total[1] - 20 * 128) <= 20 * 128 * 1e-4
+
+
+def test_weights_of_many_sequences_and_many_rows():
+    """More sequences than the plan holds in shared memory, most without rows;
+    more rows than it has threads."""
+    lens = [70 + (31 * i) % 200 for i in range(1100)]
+    x = ref.make(lens, [1 if i % 3 == 0 else 0 for i in range(1100)], 128, seed=45)
+    _, lse = _attn(x)
+    mass = dsa.mla_attn_mass_paged(*x.args(), lse, SCALE)
+    want, tol = ref.received(x, lse, torch.zeros_like(mass))
+    assert bool(((mass.double() - want).abs() <= tol).all())
+    y = ref.make([1500, 700], [1100, 300], 8, seed=46)
+    _, lse = _attn(y)
+    mass = dsa.mla_attn_mass_paged(*y.args(), lse, SCALE)
+    want, tol = ref.received(y, lse, torch.zeros_like(mass))
+    assert bool(((mass.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("heads,window,sinks", [(128, 40, 0), (128, 40, 3), (8, 300, 300), (100, 40, 700)])
+def test_weights_where_most_rows_miss_most_tiles(heads, window, sinks):
+    """A long chunk behind a short window: tiles that only some rows see, parts
+    of tiles that no row of a cluster's share sees."""
+    x = ref.make([2600, 1400], [900, 700], heads, seed=47)
+    _, lse = _attn(x, window=window, sinks=sinks)
+    mass = dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, window=window, sinks=sinks)
+    want, tol = ref.received(x, lse, torch.zeros_like(mass), window=window, sinks=sinks)
+    assert bool(((mass.double() - want).abs() <= tol).all())
+    again = dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, window=window, sinks=sinks)
+    assert torch.equal(again, mass)
 
 
 def test_weights_captured_and_replayed():

@@ -85,6 +85,15 @@ def test_select_with_ties_and_special_values(kind, n):
         _check_select(mass, [n, n - 1, n // 2 + 1], keep, sinks, recent)
 
 
+@pytest.mark.parametrize("max_len,n,offset", [(5001, 3, 0), (12000, 64, 0), (70003, 2, 1), (40000, 200, 0)])
+def test_select_at_every_alignment_and_cluster(max_len, n, offset):
+    """Rows that start on any 4-byte boundary; few and many sequences."""
+    g = torch.Generator(device="cuda").manual_seed(max_len)
+    mass = torch.rand(n, max_len, generator=g, device="cuda")
+    lens = [max_len - (i * 977) % (max_len // 2) for i in range(n)]
+    _check_select(mass, lens, max_len // 3 + offset, 3, 50)
+
+
 def test_select_captured_and_replayed():
     mass = torch.rand(4, 5000, device="cuda")
     lens = _i32([5000, 4000, 100, 3001])
