@@ -189,7 +189,7 @@ __device__ __forceinline__ Unit unit_at(const Args& a, int t)
 
 // A part as the other warps need it.
 struct PartInfo {
-    int t, rows;               // first row, (row, head) pairs
+    int t, rows;               // first row, (row, head) pairs (without keys: of any number of units)
     int hi, min_hi, max_lo, sink_end;
     int ns, m0;
     int a, nt;                 // first tile and tiles of the part; nt = 0: a unit without keys, -1: no more parts
@@ -726,7 +726,17 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 }
                 break;
             }
-            const Unit u = unit_at<32>(args, t);
+            Unit u = unit_at<32>(args, t);
+            // units without keys (padding) go as one part, however many follow one
+            // another: the softmax warps look for the next part with keys while
+            // the O warps wait for the present one, so no more than one part
+            // without keys may lie between two with
+            while (u.nt == 0 && at >= pc.w0 && at + kUnitCost < pc.w1 && t + u.n < args.T) {
+                const Unit v = unit_at<32>(args, t + u.n);
+                if (v.nt != 0) break;
+                u.n += v.n;
+                at += kUnitCost;
+            }
             bool mine = false;
             if (el) {
                 mine = part_of(args, pc, cid, u, at, infos + slot, rank == 0 ? desc + cid : nullptr);
@@ -755,9 +765,11 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             const size_t row = (size_t)p.t * args.Hq + r;
             __nv_bfloat16* orow = out + row * kDv + side * 256;
             if (p.nt == 0) {
-                if (live) {
-                    for (int v = 0; v < 32; ++v) reinterpret_cast<uint4*>(orow)[v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (side == 0) lse[row] = -INFINITY;
+                for (int rr = r; rr < p.rows; rr += kRows) {
+                    const size_t at = (size_t)p.t * args.Hq + rr;
+                    uint4* dst = reinterpret_cast<uint4*>(out + at * kDv + side * 256);
+                    for (int v = 0; v < 32; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (side == 0) lse[at] = -INFINITY;
                 }
                 __syncwarp();
                 continue;

@@ -92,6 +92,46 @@ def test_more_rows_than_the_plan_has_threads():
     ref.check_attention(y, out, lse, window=200, sinks=5)
 
 
+@pytest.mark.parametrize("heads,lens,chunks,pads", [
+    (128, [364, 370, 386], [86, 86, 86], (0, 0, 0, 5)),
+    (128, [100, 120], [40, 30], (9, 70, 33)),          # before, between and behind the sequences
+    (16, [300, 200], [20, 50], (40, 100, 300)),
+    (128, [50], [1], (0, 700)),
+    (128, [50], [1], (700, 0)),
+    (64, [9], [1], (0, 3)),
+])
+def test_stretches_of_padding(heads, lens, chunks, pads):
+    x = ref.make(lens, chunks, heads, seed=57)
+    seq, pos, at = [], [], 0
+    for b, c in enumerate(chunks + [0]):
+        seq += [-1] * pads[b] + x.seq[at:at + c].tolist()
+        pos += [-1] * pads[b] + x.pos[at:at + c].tolist()
+        at += c
+    g = torch.Generator(device="cuda").manual_seed(58)
+    x.seq = torch.tensor(seq, dtype=torch.int32, device="cuda")
+    x.pos = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    x.q = torch.randn(len(seq), heads, ref.D_QK, generator=g, device="cuda").bfloat16()
+    out = torch.full((len(seq), heads, D_V), 5.0, dtype=torch.bfloat16, device="cuda")
+    got = _attn(x, out=out)
+    ref.check_attention(x, *got)
+    mass = dsa.mla_attn_mass_paged(*x.args(), got[1], SCALE)
+    want, tol = ref.received(x, got[1], torch.zeros_like(mass))
+    assert bool(((mass.double() - want).abs() <= tol).all())
+
+
+def test_only_padding():
+    x = ref.make([64], [1], 128, seed=59)
+    x.seq = torch.full((600,), -1, dtype=torch.int32, device="cuda")
+    x.pos = torch.zeros(600, dtype=torch.int32, device="cuda")
+    x.q = torch.zeros(600, 128, ref.D_QK, dtype=torch.bfloat16, device="cuda")
+    out, lse = _attn(x)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    mass = torch.rand(1, x.S, device="cuda")
+    start = mass.clone()
+    dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, mass=mass)
+    assert torch.equal(mass, start)
+
+
 @pytest.mark.parametrize("lens", [[1000] * 40, [1000] * 39 + [1500], [1000] * 39 + [6000], [64] * 74, [64] * 75])
 def test_units_whole_or_cut(lens):
     """As many even units as clusters, one longer than the others, and one more."""
