@@ -87,10 +87,10 @@ constexpr int kUnitCost = 3;
 // Least work of a cluster: below it more clusters only add parts to join.
 constexpr int kMinWork = 8;
 // Where there are no more units than clusters and the largest is at most this
-// much above an even piece, each cluster takes a unit whole: parts written and
-// joined again cost more than the evenness gains (64 windows of 1024 keys: 48
-// us cut evenly, MEASURED whole).
-constexpr int kWholeSlack = 4;
+// much above an even piece, each cluster takes a unit whole: a second launch
+// and the parts' way through memory cost some 7 us, the time of six tiles (64
+// windows of 1024 keys: 48 us cut evenly, 33 us whole).
+constexpr int kWholeSlack = 6;
 
 // A split unit that the cluster of its last tile describes for the join.
 struct SplitDesc {
@@ -350,7 +350,7 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
             all += units[2 * w];
             largest = max(largest, units[2 * w + 1]);
         }
-        if (all <= p.ncl && largest <= p.total / p.ncl + kWholeSlack) {
+        if (all <= clusters && largest <= p.total / p.ncl + kWholeSlack) {
             // unit cid, whole; its thread alone knows where it lies
             mine = here > 0 && n_units == cid;
             p.w0 = 0;
