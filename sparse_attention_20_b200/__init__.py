@@ -385,7 +385,7 @@ def _run(fn, device, stream, *args) -> None:
 def _ints(**values) -> None:
     """Sizes that a C int has to hold (ctypes would cut them silently)."""
     for name, v in values.items():
-        if not -2 ** 31 <= v < 2 ** 31:
+        if not -0x80000000 <= v < 0x80000000:
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 
@@ -401,17 +401,36 @@ def _pages(t, name, cols=None, dtype=None, page_size=0, device=None):
     return t, t.shape[0] // page_size
 
 
+def _need(t, name, dtype, shape, device):
+    """_arg, with one test in the ordinary case (a decode step's calls take less
+    time than the checks of their arguments would)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == device.index and t.is_contiguous()):
+        _arg(t, name, dtype, shape, device)
+    return t
+
+
 def _cache_rows(q, kv_pages, page_size, block_table, seq, pos):
     """Checked operands of attention over the paged latent cache:
-    (q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, device)."""
-    q = _dev(q, "q")
-    if q.dtype != torch.bfloat16 or q.dim() != 3:
+    (num_pages, n_seqs, max_pages, T, Hq, d_qk, device)."""
+    _dev(q, "q")
+    if q.dtype is not torch.bfloat16 or q.dim() != 3:
         raise TypeError(f"q must be bfloat16 [T, Hq, d_qk], got {q.dtype} {tuple(q.shape)}")
     T, Hq, d_qk = q.shape
     dev = q.device
-    kv_pages, num_pages = _pages(kv_pages, "kv_pages", d_qk, torch.bfloat16, page_size, dev)
-    block_table, seq, pos = _paged_tables(block_table, seq, pos, T, dev)
-    return q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev
+    if not (isinstance(kv_pages, torch.Tensor) and kv_pages.dim() == 2 and page_size > 0 and
+            kv_pages.shape[0] % page_size == 0):
+        _pages(kv_pages, "kv_pages", d_qk, torch.bfloat16, page_size, dev)
+    rows = kv_pages.shape[0]
+    _need(kv_pages, "kv_pages", torch.bfloat16, (rows, d_qk), dev)
+    if not (isinstance(block_table, torch.Tensor) and block_table.dtype is torch.int32 and block_table.dim() == 2):
+        _paged_tables(block_table, seq, pos, T, dev)
+        raise TypeError("block_table must be int32 [n_seqs, max_pages]")
+    n_seqs, max_pages = block_table.shape
+    _need(block_table, "block_table", torch.int32, (n_seqs, max_pages), dev)
+    _need(seq, "seq", torch.int32, (T,), dev)
+    _need(pos, "pos", torch.int32, (T,), dev)
+    return rows // page_size, n_seqs, max_pages, T, Hq, d_qk, dev
 
 
 @functools.lru_cache(maxsize=64)
@@ -424,10 +443,14 @@ def alloc_mla_attn_workspace(T: int, Hq: int, device=None) -> torch.Tensor:
     return torch.empty(_attn_ws_bytes(T, Hq), dtype=torch.uint8, device=device or "cuda")
 
 
+@functools.lru_cache(maxsize=64)
+def _mass_ws_bytes(n_seqs: int) -> int:
+    return max(int(load_library().dsa_mla_attn_mass_paged_workspace_size(n_seqs)), 256)
+
+
 def alloc_mla_mass_workspace(n_seqs: int, device=None) -> torch.Tensor:
     """Workspace of ``mla_attn_mass_paged`` for n_seqs sequences."""
-    n = int(load_library().dsa_mla_attn_mass_paged_workspace_size(n_seqs))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_mass_ws_bytes(n_seqs), dtype=torch.uint8, device=device or "cuda")
 
 
 def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: float, d_v: int, window: int = 0,
@@ -438,17 +461,15 @@ def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: fl
     the first `sinks`. A row without keys gives out = 0, lse = -inf.
 
     Buffers not given are allocated on the stream that the call runs on."""
-    q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
-                                                                                  block_table, seq, pos)
+    num_pages, n_seqs, max_pages, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size, block_table, seq, pos)
     _ints(window=window, sinks=sinks, page_size=page_size)
     lib = load_library()
     out = _new((T, Hq, d_v), torch.bfloat16, dev, stream) if out is None else \
-        _arg(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
+        _need(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
     lse = _new((T, Hq), torch.float32, dev, stream) if lse is None else \
-        _arg(lse, "lse", torch.float32, (T, Hq), dev)
+        _need(lse, "lse", torch.float32, (T, Hq), dev)
     if workspace is None:
         workspace = _new(_attn_ws_bytes(T, Hq), torch.uint8, dev, stream)
-    n_seqs, max_pages = block_table.shape
     _run(lib.dsa_mla_attn_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages, page_size,
          block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), T, Hq, d_qk, d_v, scale, window,
          sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
@@ -463,17 +484,15 @@ def mla_attn_mass_paged(q, kv_pages, page_size: int, block_table, seq, pos, lse,
     lse is ``mla_attn_paged``'s for the same rows, window and sinks. mass is
     accumulated into (a new zeroed tensor when None). workspace: see
     ``alloc_mla_mass_workspace``."""
-    q, kv_pages, num_pages, block_table, seq, pos, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size,
-                                                                                  block_table, seq, pos)
+    num_pages, n_seqs, max_pages, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size, block_table, seq, pos)
     _ints(window=window, sinks=sinks, page_size=page_size)
-    _arg(lse, "lse", torch.float32, (T, Hq), dev)
-    n_seqs, max_pages = block_table.shape
+    _need(lse, "lse", torch.float32, (T, Hq), dev)
     shape = (n_seqs, max_pages * page_size)
     mass = _new(shape, torch.float32, dev, stream, zero=True) if mass is None else \
-        _arg(mass, "mass", torch.float32, shape, dev)
+        _need(mass, "mass", torch.float32, shape, dev)
     lib = load_library()
     if workspace is None:
-        workspace = _new(lib.dsa_mla_attn_mass_paged_workspace_size(n_seqs), torch.uint8, dev, stream)
+        workspace = _new(_mass_ws_bytes(n_seqs), torch.uint8, dev, stream)
     _run(lib.dsa_mla_attn_mass_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages,
          page_size, block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), lse.data_ptr(), T, Hq,
          d_qk, scale, window, sinks, mass.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
