@@ -365,26 +365,52 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     const int col = y * slice, width = min(slice, mv.bytes - col), pieces = width / 16;
     const int rows = min(max_rows, shape.buf / width);             // of a block, in one CTA
     const int* bt = pg.block_table + (size_t)b * pg.max_pages;
-    auto pool_row = [&](int s) -> int {
-        const int page = bt[s / pg.page_size];
-        return (unsigned)page < (unsigned)pg.num_pages ? page * pg.page_size + s % pg.page_size : -1;
-    };
     uint8_t* base = mv.rows + col;
     const int per = size * rows;
     const int blocks = (m + per - 1) / per;
-    // where block k's rows of this CTA come from and go
-    auto look_up = [&](int k) {
+    // Where block k's rows of this CTA come from and go, in three steps that lie
+    // an iteration of the loop apart, or the stores of a block, so that no
+    // thread waits for its loads: positions, their pages, the table.
+    static_assert(kMoveThreads * 2 >= 1024, "rows of a block per thread");
+    int pos_of[2];                       // the kept position, -1: none or stays
+    int page_from[2], page_to[2], at_from[2], at_to[2];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = tid + i * kMoveThreads, j = (k * size + rank) * rows + r;
+            const int s = r < rows && j < m ? idx[j] : -1;
+            pos_of[i] = s > j && s < S ? s : -1;
+        }
+    };
+    auto find = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (pos_of[i] < 0) continue;
+            const int j = (k * size + rank) * rows + tid + i * kMoveThreads;
+            const int pf = pos_of[i] / pg.page_size, pt = j / pg.page_size;
+            at_from[i] = pos_of[i] - pf * pg.page_size;
+            at_to[i] = j - pt * pg.page_size;
+            page_from[i] = bt[pf];
+            page_to[i] = bt[pt];
+        }
+    };
+    auto note = [&](int k) {
         int2* ft = from_to + (k % 3) * max_rows;
-        for (int r = tid; r < rows; r += kMoveThreads) {
-            const int j = (k * size + rank) * rows + r;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = tid + i * kMoveThreads;
+            if (r >= rows) continue;
             int2 f = make_int2(-1, -1);
-            if (j < m) {
-                const int s = idx[j];
-                if (s > j && s < S) f = make_int2(pool_row(s), pool_row(j));
-                if (f.y < 0) f.x = -1;
-            }
+            if (pos_of[i] >= 0 && (unsigned)page_from[i] < (unsigned)pg.num_pages &&
+                (unsigned)page_to[i] < (unsigned)pg.num_pages)
+                f = make_int2(page_from[i] * pg.page_size + at_from[i], page_to[i] * pg.page_size + at_to[i]);
             ft[r] = f;
         }
+    };
+    auto look_up = [&](int k) {
+        fetch(k);
+        find(k);
+        note(k);
     };
     // this thread's piece of every step-th row
     const int step = kMoveThreads / pieces, r_first = tid / pieces, p = tid - r_first * pieces;
@@ -400,6 +426,7 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
     __syncthreads();
     if (blocks > 0) read(0);
     if (blocks > 1) look_up(1);
+    if (blocks > 2) fetch(2);
     for (int k = 0; k < blocks; ++k) {
         // block k is read everywhere: its copies have landed, so the barrier need
         // not order anything (a release waits for the last block's stores)
@@ -407,7 +434,7 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
         __syncthreads();
         if (size > 1) sm100::cluster_sync_relaxed();
         if (k + 1 < blocks) read(k + 1);
-        if (k + 2 < blocks) look_up(k + 2);
+        if (k + 2 < blocks) find(k + 2);
         const int2* ft = from_to + (k % 3) * max_rows;
         const uint8_t* src = buf + (k & 1) * shape.buf + p * 16;
         if (r_first < step)
@@ -415,6 +442,8 @@ cache_compact_kernel(const MoveRows kv, const MoveRows keys, float* __restrict__
                 if (ft[r].x >= 0)
                     *reinterpret_cast<uint4*>(base + (size_t)ft[r].y * mv.bytes + p * 16) =
                         *reinterpret_cast<const uint4*>(src + r * width);
+        if (k + 2 < blocks) note(k + 2);
+        if (k + 3 < blocks) fetch(k + 3);
     }
 }
 
