@@ -63,8 +63,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums)
 // is added up in the first CTA (only the bins in use cross the cluster), which
 // names the digit. A CTA keeps the order keys of its first 11776 positions in
 // shared memory, so that four CTAs share a SM and 64 sequences of any length
-// run at once (with 16384 it is three, and the second round of the card took
-// as long as the first: 46 us against MEASURED); the others are read again for each
+// run at once (with 16384 it is three and two rounds of the card: 46 us
+// against 43); the others are read again for each
 // pass. Work is bound by instructions, so positions are handled four a lane,
 // and protected ones are left out by an order key of 0, which no weight has.
 __global__ void __launch_bounds__(kSelThreads, 4)
@@ -273,14 +273,15 @@ struct MoveShape {
     size_t smem() const { return 2 * (size_t)buf + 3 * (size_t)rows * 8; }
 };
 
-// All CTAs should run at once (352 CTAs on 296 places took 80 us for what 256
-// take MEASURED), with 7.5 MB in flight to fill HBM, and in few blocks, each of
-// which costs some 2.5 us of latency: one sequence's 16384 rows in two blocks of
-// 96 KB per CTA, one CTA a SM; 32 sequences' 4099 rows in 40 KB, two CTAs a SM.
+// All CTAs should run at once, with 7.5 MB in flight to fill HBM, and in few
+// blocks, each of which costs some 2.5 us of latency. One sequence's 16384 rows
+// go in two blocks of 96 KB per CTA, one CTA a SM (14 us; in 40 KB, two a SM, 18);
+// 32 sequences' 4099 rows in 48 KB, two CTAs a SM, slices of 192 bytes: 66 us,
+// 5.2 TB/s (in 24 KB 86, slices of 384 bytes 95, of 96 bytes 80).
 inline MoveShape move_shape(int n_seqs, int kv_bytes, int k_bytes, bool mass, int keep, int sms)
 {
     static const int cuts[] = {1, 2, 3, 4, 6, 9, 12, 18};
-    MoveShape best = {128, 1, 40 * 1024, 640};
+    MoveShape best = {128, 1, 48 * 1024, 512};
     double best_us = 1e30;
     long long best_total = 0;
     for (int resident = 1; resident <= 2; ++resident)
@@ -289,8 +290,8 @@ inline MoveShape move_shape(int n_seqs, int kv_bytes, int k_bytes, bool mass, in
                 MoveShape m;
                 m.slice = ((kv_bytes + n - 1) / n + 31) / 32 * 32;
                 m.size = size;
-                m.buf = resident == 1 ? 96 * 1024 : 40 * 1024;
-                m.rows = resident == 1 ? 1024 : 640;
+                m.buf = resident == 1 ? 96 * 1024 : 48 * 1024;
+                m.rows = resident == 1 ? 1024 : 512;
                 if (m.slice < 64 && n > 1) continue;
                 const long long total = (long long)n_seqs * size *
                                         (ceil_div(kv_bytes, m.slice) + ceil_div(k_bytes, m.slice) + (mass ? 1 : 0));

@@ -54,9 +54,12 @@ constexpr int kAhead = 4;                                 // steps handed out ah
 constexpr int kOffCol = kOffBar + 512;                    // [kAhead][256] lse2, last and first key seen
 constexpr int kOffHalf = kOffCol + kAhead * 3 * kPairs * 4;   // [kAhead][128] sums of the second column half
 constexpr int kOffStep = kOffHalf + kAhead * 128 * 4;          // [kAhead] StepInfo
-constexpr int kSmem = kOffStep + kAhead * 64 + 1024;
-static_assert(kSmem <= 232448, "shared memory");
-
+// Up to this many sequences every CTA makes the plan itself, in its shared
+// memory; a kernel before it takes 5 us and the time between two launches.
+constexpr int kNearSeqs = 64;
+constexpr int kOffHead = kOffStep + kAhead * 64;
+constexpr int kOffSeqs = kOffHead + 320;
+constexpr int kSmem = kOffSeqs + kNearSeqs * 32 + 1024;
 enum : int {
     B_KFULL = 0, B_KEMPTY = 9, B_QFULL = 18, B_QEMPTY = 22, B_DFULL = 26, B_DFREE = 28, B_STEP = 30,
     B_STEPFREE = 34, B_HALF = 38, B_DRAIN = 42, B_COUNT = 43
@@ -83,14 +86,16 @@ struct Header {
 struct SplitTile {
     int b, tile;                 // b < 0: none
     int c_first, c_last;
-    long long base;
-    long long pad;
+    long long base, total;
+    int ncl, pad;
 };
+
+static_assert(kSmem <= 232448, "shared memory");
 
 constexpr size_t kHeaderBytes = 512;
 constexpr size_t kDescBytes = kMaxClusters * sizeof(SplitTile);
 constexpr size_t kPartBytes = (size_t)kMaxClusters * 2 * kTile * 4;
-static_assert(sizeof(Header) <= kHeaderBytes, "header");
+static_assert(sizeof(Header) <= 320 && sizeof(SeqPlan) == 32 && 320 <= kHeaderBytes, "header");
 constexpr size_t kFixedBytes = (kHeaderBytes + kDescBytes + kPartBytes + 255) / 256 * 256;
 
 __host__ __device__ __forceinline__ size_t ws_bytes(int n_seqs) { return kFixedBytes + (size_t)n_seqs * sizeof(SeqPlan); }
@@ -138,36 +143,29 @@ __device__ __forceinline__ int steps_of(const SeqPlan& s, int Hq)
 __device__ __forceinline__ long long piece_begin(long long total, int ncl, int c) { return total * c / ncl; }
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 1024;     // sequences that the plan kernel handles in shared memory
 
-constexpr int kPlanSeqs = 1024;     // sequences that the plan handles in shared memory
-
-// One CTA: rows and keys of each sequence, then the line of work.
-__global__ void __launch_bounds__(kPlanThreads)
-cache_mass_plan_kernel(const Args a, int clusters, void* ws)
+// A block of `threads` threads: rows and keys of each sequence, then the line
+// of work, into w.head and w.seqs; seqs is where it works (w.seqs or shared
+// memory), wsum a shared word pair per warp.
+template <int threads>
+__device__ void plan_block(const Args& a, int clusters, const Ws& w, volatile SeqPlan* seqs, long long* wsum)
 {
-    __shared__ long long wsum[32];
-    __shared__ SeqPlan near[kPlanSeqs];
-    const Ws w = ws_of(ws);
-    volatile SeqPlan* seqs = a.pg.n_seqs <= kPlanSeqs ? near : w.seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_wait();
-    for (int b = tid; b < a.pg.n_seqs; b += kPlanThreads) {
+    for (int b = tid; b < a.pg.n_seqs; b += threads) {
         seqs[b].t_min = seqs[b].lo = INT_MAX;
         seqs[b].t_max = seqs[b].hi = -1;
     }
-    for (int c = tid; c < clusters; c += kPlanThreads) w.desc[c].b = -1;
     __syncthreads();
     const int sink_end = a.window > 0 ? a.sinks : 0;
-    for (int t0 = 0; t0 < a.T; t0 += kPlanThreads) {
+    for (int t0 = 0; t0 < a.T; t0 += threads) {
         const int t = t0 + tid;
         int b = -1, hi = -1, lo = INT_MAX;
         if (t < a.T) {
-            long long base;
-            const int* bt;
-            const int n = row_keys(a.pg, a.pos, nullptr, t, a.T, 0, &base, &bt);
-            if (n > 0) {
-                const Visible v = visible_of(n, a.pos[t], a.window, a.sinks);
-                b = a.pg.seq[t];
+            Visible v;
+            const int sq = a.pg.seq[t];
+            if (cache_attn::row_sees(a, sq, a.pos[t], v)) {
+                b = sq;
                 hi = v.hi;
                 lo = v.lo;
             }
@@ -191,7 +189,7 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
         }
     }
     __syncthreads();
-    const int per = ceil_div(a.pg.n_seqs, kPlanThreads);
+    const int per = ceil_div(a.pg.n_seqs, threads);
     const int b0 = min(a.pg.n_seqs, tid * per), b1 = min(a.pg.n_seqs, b0 + per);
     auto cost = [&](int b) -> long long {
         SeqPlan s;
@@ -210,7 +208,8 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
     if (lane == 31) wsum[warp] = pre;
     __syncthreads();
     long long base = 0, total = 0;
-    for (int i = 0; i < 32; ++i) {
+#pragma unroll
+    for (int i = 0; i < threads / 32; ++i) {
         if (i < warp) base += wsum[i];
         total += wsum[i];
     }
@@ -222,7 +221,7 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
     }
     for (int b = b0; b < b1; ++b) {
         const long long c = cost(b);
-        if (a.pg.n_seqs <= kPlanSeqs) {
+        if (seqs != w.seqs) {
             SeqPlan s;
             s.t_min = seqs[b].t_min;
             s.t_max = seqs[b].t_max;
@@ -250,6 +249,18 @@ cache_mass_plan_kernel(const Args a, int clusters, void* ws)
         }
         w.head->first[tid] = l;
     }
+}
+
+// For more sequences than each CTA of the main kernel plans for itself.
+__global__ void __launch_bounds__(kPlanThreads)
+cache_mass_plan_kernel(const Args a, int clusters, void* ws)
+{
+    __shared__ long long wsum[32];
+    __shared__ SeqPlan near[kPlanSeqs];
+    griddep_launch();
+    griddep_wait();
+    const Ws w = ws_of(ws);
+    plan_block<kPlanThreads>(a, clusters, w, a.pg.n_seqs <= kPlanSeqs ? near : w.seqs, wsum);
 }
 
 // What row t sees if it belongs to sequence b (false: nothing).
@@ -414,6 +425,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
     const uint32_t rank = cluster_ctarank();
     const int cid = (int)(blockIdx.x >> 1);
 
+    griddep_launch();
     if (threadIdx.x == 0) {
         for (int k = 0; k < kSlabs; ++k) {
             mbar_init(bar(B_KFULL + k), 1);
@@ -447,7 +459,15 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
     griddep_wait();
     const uint32_t tmem = *taddr_slot;
     const uint32_t el = elect_one();
-    const Ws ws = ws_of(ws_raw);
+    Ws ws = ws_of(ws_raw);
+    if (args.pg.n_seqs <= kNearSeqs) {
+        ws.head = reinterpret_cast<Header*>(sgen + kOffHead);
+        ws.seqs = reinterpret_cast<SeqPlan*>(sgen + kOffSeqs);
+        plan_block<kThreads>(args, (int)(gridDim.x >> 1), ws, ws.seqs,
+                             reinterpret_cast<long long*>(sgen + kOffBar + 384));
+    }
+    if (rank == 0 && threadIdx.x == 0) ws.desc[cid].b = -1;
+    __syncthreads();
     bool issued_any = false;
     // pairs of a step as the MMA's N
     auto n_of = [&](const Step& s) -> int { return s.n * args.Hq > 128 ? 256 : 128; };
@@ -652,6 +672,8 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                         d.c_first = (int)(((cur.base + kTileCost + 1) * walk.ncl - 1) / walk.total);
                         d.c_last = cid;
                         d.base = cur.base;
+                        d.total = walk.total;
+                        d.ncl = walk.ncl;
                         d.pad = 0;
                         ws.desc[cid] = d;
                     }
@@ -792,15 +814,14 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
 __global__ void __launch_bounds__(kTile)
 cache_mass_join_kernel(const void* ws_raw, int S, float* __restrict__ mass)
 {
+    griddep_launch();
     griddep_wait();
     const Ws w = ws_of(const_cast<void*>(ws_raw));
     const SplitTile d = w.desc[blockIdx.x];
     if (d.b < 0) return;
-    const long long total = w.head->total;
-    const int ncl = w.head->ncl;
     float sum = 0.f;
     for (int c = d.c_first; c <= d.c_last; ++c)
-        sum += w.parts[((size_t)c * 2 + (d.base < piece_begin(total, ncl, c) ? 0 : 1)) * kTile + threadIdx.x];
+        sum += w.parts[((size_t)c * 2 + (d.base < piece_begin(d.total, d.ncl, c) ? 0 : 1)) * kTile + threadIdx.x];
     const int key = d.tile + (int)threadIdx.x;
     if (key < S && sum != 0.f) mass[(size_t)d.b * S + key] += sum;
 }

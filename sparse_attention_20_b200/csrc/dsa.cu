@@ -1327,8 +1327,10 @@ int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, 
     const Args args = cache_attn_args(pg, pos, T, Hq, window, sinks);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int clusters = std::min(kMaxClusters, std::max(1, num_sms() / 2));
-    launch_pdl(cache_mass_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, args, clusters, workspace);
-    DSA_LAUNCH_CHECK("cache_mass_plan_kernel");
+    if (n_seqs > kNearSeqs) {
+        launch_pdl(cache_mass_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, args, clusters, workspace);
+        DSA_LAUNCH_CHECK("cache_mass_plan_kernel");
+    }
     launch_pdl(cache_mass_tc_kernel, dim3(2 * clusters), dim3(kThreads), kSmem, st, tk, tq128, tq64, lse, args,
                scale * 1.4426950408889634f, workspace, mass);
     DSA_LAUNCH_CHECK("cache_mass_tc_kernel");
