@@ -12,14 +12,14 @@
 // tensor memory, and the logits need no exchange. Per tile: S = Q C^T takes 36
 // MMAs of N = 128 (each CTA brings 64 of the keys, all 576 columns), O += P
 // C[:, 0:512] takes 16 of N = 256 (each CTA brings all 128 keys, its 256
-// columns). An N = 128 pair MMA takes 44.6 clocks here and an N = 256 one 64
-// (measured), whether A lies in TMEM or shared memory: 2630 clocks a tile,
-// 0.83 of the tensor pipe's peak. Keys cross L2 twice a tile (72 + 64 KB per
+// columns): 32 and 64 clocks each (measured, A in TMEM or shared memory alike), 2176
+// a tile, the tensor pipe's rate. Keys cross L2 twice a tile (72 + 64 KB per
 // CTA); box loads of 24 to 32 KB reach 85 B/clk/SM from L2 and 7.4 TB/s from
 // HBM, single 8 KB ones 22 B/clk, so a tile is loaded in boxes of four slabs of
 // 64 columns x 64 keys, through one ring in the order the MMAs consume:
-//   Q K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1)
-// so a unit's Q is on its way while the unit before it ends. While the softmax of tile j runs, the tensor pipe does PV(j-1) and QK(j+1).
+//   Q K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) Q' K'(0) V(n-1) K'(1) V'(0) ...
+// that runs on across units. While the softmax of tile j runs, the tensor pipe
+// does PV(j-1) and QK(j+1), of the next unit if need be.
 //
 // Work is split evenly over the clusters: the units' tiles lie on one line
 // (with a constant per unit for its Q and its epilogue) that is cut into equal
@@ -32,9 +32,12 @@
 // shared memory before PV (a row that does see the key has a NaN logit).
 //
 // Warps (16 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
-// keys each) and Q; 8 loads; 9 MMA issue (even CTA); 10 walks the cluster's
-// piece and hands its parts to the others; 12-15 take O out of TMEM and write
-// it, while the softmax is at the next unit already.
+// keys each); 8 loads; 9 MMA issue (even CTA); 10 walks the cluster's piece and
+// hands its parts to the others; 12-15 bring a unit's Q into TMEM as soon as
+// the last QK of the unit before is done, and take O out and write it, while
+// the softmax is at the next unit already. (With Q written by the softmax
+// warps behind a unit's last tile a unit of 386 keys took 17000 clocks, so
+// 13500; the O warps' 64 KB, 5000 clocks of scattered stores, bound it now.)
 #pragma once
 #include <cuda.h>
 
@@ -72,13 +75,13 @@ static_assert(kTcSmem <= 232448, "shared memory");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
 // On the even CTA's barriers: FULL, RFULL (bytes of both CTAs), QT, SFREE, PFULL
-// OFREE (arrivals of both). OWN: a slot that the softmax warps look at first (a unit's
-// Q, the values of a tile that not every row sees whole), QROPE: Q's last
-// slab, on each CTA's own.
+// OFREE (arrivals of both). OWN: a slot that the softmax warps look at first
+// (the values of a tile that not every row sees whole), QLOAD: a unit's Q, on
+// each CTA's own.
 enum : int {
     B_FULL = 0, B_EMPTY = 5, B_OWN = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
-    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QROPE = 28,
-    B_OFREE = 29, B_PART = 30, B_PARTFREE = 34, B_COUNT = 38
+    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QLOAD = 28,
+    B_OFREE = 30, B_PART = 31, B_PARTFREE = 35, B_QFREE = 39, B_COUNT = 40
 };
 
 constexpr int kMaxClusters = 74;
@@ -462,16 +465,20 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             mbar_init(bar(B_REMPTY + b), 1);
             mbar_init(bar(B_RED + b), 8);
         }
-        // the softmax warps of both CTAs
-        mbar_init(bar(B_QT), 16);
+        // the softmax warps, and those of Q and O, of both CTAs
         mbar_init(bar(B_SFREE), 16);
         mbar_init(bar(B_PFULL), 16);
-        mbar_init(bar(B_OFREE), 8);             // the warps that read O, of both CTAs
+        mbar_init(bar(B_QT), 8);
+        mbar_init(bar(B_OFREE), 8);
+        mbar_init(bar(B_QFREE), 1);
         mbar_init(bar(B_SFULL), 1);
         mbar_init(bar(B_PVDONE), 1);
         mbar_init(bar(B_LSUM), 8);
         mbar_init(bar(B_DRAIN), 1);
-        mbar_init(bar(B_QROPE), 1);
+        // of every other unit each (a unit's Q may be on its way before the last one's
+        // is here): two slots and a rope slot
+        mbar_init(bar(B_QLOAD), 3);
+        mbar_init(bar(B_QLOAD + 1), 3);
         for (int p = 0; p < kAhead; ++p) {
             mbar_init(bar(B_PART + p), 1);
             mbar_init(bar(B_PARTFREE + p), rank == 0 ? 14 : 13);   // softmax, loads, MMA issue, O
@@ -516,17 +523,17 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         uint32_t ph = 0, rph = 0;
         bool ok = true;
         const uint32_t full0 = mapa(bar(B_FULL), 0), rfull0 = mapa(bar(B_RFULL), 0);
-        // one box of four slabs (columns 64 * z ..) of 64 rows from `row`; for own
-        // the softmax warps wait for it and the MMA for them
-        auto push = [&](const CUtensorMap* tm, int row, int z, bool own) {
+        // one box of four slabs (columns 64 * z ..) of 64 rows from `row`; with a
+        // barrier of this CTA the warps that wait there look at it before the MMA
+        auto push = [&](const CUtensorMap* tm, int row, int z, uint32_t own) {
             if (!ok) return;
             ok = wait_lanes(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, n);
             if (!ok) return;
             if (el) {
                 const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
                 if (own) {
-                    mbar_arrive_expect_tx(bar(B_OWN + slot), kSlotBytes);
-                    tma_load_3d(dst, tm, 0, row, z, bar(B_OWN + slot));
+                    mbar_arrive_expect_tx(own, kSlotBytes);
+                    tma_load_3d(dst, tm, 0, row, z, own);
                     if (rank == 0) mbar_arrive(bar(B_FULL + slot));
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + slot), 2 * kSlotBytes);
@@ -540,15 +547,15 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             }
         };
         // the last slab (the rope columns)
-        auto push_rope = [&](const CUtensorMap* tm, int row, bool own) {
+        auto push_rope = [&](const CUtensorMap* tm, int row, uint32_t own) {
             if (!ok) return;
             ok = wait_lanes(bar(B_REMPTY + rslot), rph ^ 1u, abort_flag, 1010 + rslot, n);
             if (!ok) return;
             if (el) {
                 const uint32_t dst = sbase + kOffRope + rslot * kSlab;
                 if (own) {
-                    mbar_arrive_expect_tx(bar(B_QROPE), kSlab);
-                    tma_load_3d(dst, tm, 0, row, 8, bar(B_QROPE));
+                    mbar_arrive_expect_tx(own, kSlab);
+                    tma_load_3d(dst, tm, 0, row, 8, own);
                     if (rank == 0) mbar_arrive(bar(B_RFULL + rslot));
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_RFULL + rslot), 2 * kSlab);
@@ -560,18 +567,25 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (rslot == 0) rph ^= 1u;
         };
         PartInfo p;
+        int units = 0, pa = 0, pb = 0;   // the last tile's cache rows, its values still to be loaded
+        bool pcut = false, before = false;
+        const int z = 4 * (int)rank;
+        auto push_values = [&]() {
+            push(&tm_kv4, pa, z, pcut ? bar(B_OWN + slot) : 0u);
+            push(&tm_kv4, pb, z, pcut ? bar(B_OWN + slot) : 0u);
+        };
         for (int np = 0; ok; ++np) {
             if (!(ok = take_part(np, p)) || p.nt < 0) break;
             if (p.nt == 0) continue;
             // this CTA's 64 of the unit's pairs (rows behind the last are read as zeros)
             const int qrow = p.t * args.Hq + (int)rank * 64;
-            push(&tm_q4, qrow, 0, true);
-            push(&tm_q4, qrow, 4, true);
-            push_rope(&tm_q1, qrow, true);
+            const uint32_t here = bar(B_QLOAD + (units++ & 1));
+            push(&tm_q4, qrow, 0, here);
+            push(&tm_q4, qrow, 4, here);
+            push_rope(&tm_q1, qrow, here);
             // cache rows of the tiles' two blocks of 64 keys, sixteen tiles at a
             // time over the lanes (a block behind the last key reads the one before)
-            int rows_l = 0, pa = 0, pb = 0;
-            bool pcut = false;
+            int rows_l = 0;
             for (int j = 0; j < p.nt && ok; ++j, ++n) {
                 if ((j & 15) == 0) {
                     int s = p.key0(min(j + (lane >> 1), p.nt - 1)) + (lane & 1) * 64;
@@ -580,25 +594,18 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 }
                 const int e = (j & 15) * 2;
                 const int ra = __shfl_sync(0xffffffffu, rows_l, e), rb = __shfl_sync(0xffffffffu, rows_l, e + 1);
-                const bool cut = !p.all_see(p.key0(j), kTile);
                 const int own = rank ? rb : ra;
-                push(&tm_kv4, own, 0, false);
-                push(&tm_kv4, own, 4, false);
-                push_rope(&tm_kv1, own, false);
-                const int z = 4 * (int)rank;
-                if (j > 0) {
-                    push(&tm_kv4, pa, z, pcut);
-                    push(&tm_kv4, pb, z, pcut);
-                }
-                if (j == p.nt - 1) {
-                    push(&tm_kv4, ra, z, cut);
-                    push(&tm_kv4, rb, z, cut);
-                }
+                push(&tm_kv4, own, 0, 0u);
+                push(&tm_kv4, own, 4, 0u);
+                push_rope(&tm_kv1, own, 0u);
+                if (before) push_values();
+                before = true;
                 pa = ra;
                 pb = rb;
-                pcut = cut;
+                pcut = !p.all_see(p.key0(j), kTile);
             }
         }
+        if (before) push_values();
         if (!ok) {
             // given up: copies in flight land before the CTA gives its shared memory up
             const uint64_t t0 = globaltimer_ns();
@@ -613,7 +620,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         const uint64_t d_r = smem_desc(sbase + kOffRope, 16, 1024, kSwizzle128B);
         const uint64_t d_q = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
         const uint64_t d_p = smem_desc(sbase + kOffP, 16, 1024, kSwizzle128B);
-        int slot = 0, rslot = 0, g = 0, n_units = 0;
+        int slot = 0, rslot = 0, g = 0, n_units = 0, last_nt = 0;
         uint32_t ph = 0, rph = 0;
         bool ok = true;
         // lane 0 waits for the slot, lanes 1 and 2 for other barriers (par > 1: none)
@@ -668,12 +675,13 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             mma_commit_pair(bar(B_SFULL), el);
             return true;
         };
-        // O (+)= P C[:, 0:512] of tile gp; a unit's first waits until the last unit's O is read
-        auto pv = [&](int gp, bool first) -> bool {
+        // O (+)= P C[:, 0:512] of tile gp of unit `of`, whose first waits until the O of
+        // the unit before is read
+        auto pv = [&](int gp, bool first, int of) -> bool {
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
                 if (!ready(B_PFULL, blk == 0 ? (uint32_t)(gp & 1) : 2u, 1240, B_OFREE,
-                           blk == 0 && first && n_units > 0 ? (uint32_t)((n_units - 1) & 1) : 2u))
+                           blk == 0 && first && of > 0 ? (uint32_t)((of - 1) & 1) : 2u))
                     return false;
                 tc_fence_after();
                 const uint64_t b = d_v + (uint64_t)(slot * (kSlotBytes >> 4));
@@ -694,7 +702,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (!(ok = take_part(np, p)) || p.nt < 0) break;
             if (p.nt == 0) continue;
             ok = wait_lanes(bar(B_QT), n_units & 1, abort_flag, 1250, n_units);
-            // the softmax warps have taken Q out of its two slots and rope slot
+            // Q has been taken out of its two slots and rope slot
             done();
             done();
             mma_commit_pair(bar(B_REMPTY + rslot), el);
@@ -702,12 +710,14 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (rslot == 0) rph ^= 1u;
             for (int j = 0; j < p.nt && ok; ++j) {
                 ok = qk();
+                if (j == p.nt - 1) mma_commit_pair(bar(B_QFREE), el);
+                if (ok && g > 0) ok = j > 0 ? pv(g - 1, j == 1, n_units) : pv(g - 1, last_nt == 1, n_units - 1);
                 ++g;
-                if (ok && j > 0) ok = pv(g - 2, j == 1);
             }
-            if (ok) ok = pv(g - 1, p.nt == 1);
+            last_nt = p.nt;
             ++n_units;
         }
+        if (ok && n_units > 0) ok = pv(g - 1, last_nt == 1, n_units - 1);
         // the last signals of the other CTA
         if (ok && n_units > 0)
             wait_lanes(lane == 0 ? bar(B_SFREE) : bar(B_OFREE), lane == 0 ? (uint32_t)((g - 1) & 1) : (uint32_t)((n_units - 1) & 1),
@@ -747,24 +757,54 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             t += u.n;
         }
     } else if (warp >= 12) {
-        // ---------------------------------------------------------- O out
-        // lane i holds pair i % 64 of this CTA's 64: columns 0..255 for i < 64, the
-        // others for i >= 64
+        // ------------------------------------------------------- Q in, O out
+        // lane i holds pair i % 64 of this CTA's 64: of O columns 0..255 for i < 64,
+        // the others for i >= 64
         const int i = (warp & 3) * 32 + lane, side = i >> 6, lr = i & 63;
         const int r = (int)rank * 64 + lr;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const float* lsum_s = reinterpret_cast<const float*>(sgen + kOffLsum);
         const float* max_s = reinterpret_cast<const float*>(sgen + kOffMax);
-        const uint32_t ofree0 = mapa(bar(B_OFREE), 0);
+        const uint32_t ofree0 = mapa(bar(B_OFREE), 0), qt0 = mapa(bar(B_QT), 0);
         const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        PartInfo p;
-        int uc = 0, g = 0;
-        for (int np = 0;; ++np) {
-            if (!take_part(np, p) || p.nt < 0) break;
-            const bool live = r < p.rows;
-            const size_t row = (size_t)p.t * args.Hq + r;
-            __nv_bfloat16* orow = out + row * kDv + side * 256;
-            if (p.nt == 0) {
+        int ring = 0, rope = 0;   // where Q of the next unit lies
+        // Q of unit number `units`: columns [0, 384) go to TMEM (row i % 64 in both
+        // lanes), the others to their place in shared memory
+        auto write_q = [&](int units) -> bool {
+            if (!wait_all(bar(B_QLOAD + (units & 1)), (units >> 1) & 1, abort_flag, 1336, units)) return false;
+            const uint32_t q0 = sbase + kOffRing + ring % kSlots * kSlotBytes;
+            const uint32_t q1 = sbase + kOffRing + (ring + 1) % kSlots * kSlotBytes;
+#pragma unroll 2
+            for (int sl = 0; sl < 6; ++sl) {
+                const uint32_t src = (sl < 4 ? q0 + sl * kSlab : q1 + (sl - 4) * kSlab) + lr * 128;
+                uint32_t w[32];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    const uint4 x = ld_shared_v4(src + ((v ^ (lr & 7)) << 4));
+                    w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
+                }
+                tmem_st32(tmem + lane_addr + kColQ + 32 * sl, w);
+            }
+#pragma unroll 4
+            for (int it = 0; it < 12; ++it) {
+                const uint32_t o = (uint32_t)(it & 3) * 2048 + i * 16;
+                const uint32_t src = it < 8 ? q1 + (2 + (it >> 2)) * kSlab : sbase + kOffRope + (rope & 1) * kSlab;
+                st_shared_v4(sbase + kOffQ + (it >> 2) * kSlab + o, ld_shared_v4(src + o));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(qt0);
+            return true;
+        };
+        // the next part with keys; zeros for those without
+        int np = 0;
+        bool ok = true;
+        auto advance = [&](PartInfo& p) -> bool {
+            while (true) {
+                if (!(ok = take_part(np++, p)) || p.nt < 0) return false;
+                if (p.nt > 0) return true;
                 for (int rr = r; rr < p.rows; rr += kRows) {
                     const size_t at = (size_t)p.t * args.Hq + rr;
                     uint4* dst = reinterpret_cast<uint4*>(out + at * kDv + side * 256);
@@ -772,8 +812,25 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                     if (side == 0) lse[at] = -INFINITY;
                 }
                 __syncwarp();
-                continue;
             }
+        };
+        PartInfo p, pn;
+        int uc = 0, g = 0;
+        bool have = advance(p);
+        if (have) ok = write_q(0);
+        while (have && ok) {
+            const bool more = advance(pn);
+            if (!ok) break;
+            // ring places: the values of a unit's last tile lie behind the next unit's
+            // Q and first keys (the first unit has none before it)
+            ring += 4 * p.nt + (uc > 0 ? 2 : 0);
+            rope += 1 + p.nt;
+            if (more) {
+                if (!wait_all(bar(B_QFREE), uc & 1, abort_flag, 1338, uc) || !write_q(uc + 1)) break;
+            }
+            const bool live = r < p.rows;
+            const size_t row = (size_t)p.t * args.Hq + r;
+            __nv_bfloat16* orow = out + row * kDv + side * 256;
             g += p.nt;
             // row sum over the four threads of the row
             if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g)) break;
@@ -791,6 +848,12 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 tmem_ld32(tmem + lane_addr + kColO + h0, o2[0]);
                 tmem_ld32(tmem + lane_addr + kColO + h0 + 32, o2[1]);
                 tmem_wait_ld();
+                if (h0 == 192) {
+                    // O is in registers (so the signal need not order the loads)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(ofree0);
+                }
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const uint32_t (&o)[32] = o2[hh];
@@ -822,20 +885,18 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 }
                 __syncwarp();
             }
-            // the loads' results are here, so the signal need not order them
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(ofree0);
             if (live && side == 0) {
                 if (p.place >= 0)
                     part_lse[(size_t)p.place * kRows + r] = lv;
                 else
                     lse[row] = lv * 0.69314718055994531f;
             }
+            p = pn;
+            have = more;
             ++uc;
         }
     } else if (warp < 8) {
-        // ----------------------------------------------------- softmax, Q
+        // -------------------------------------------------------- softmax
         // TMEM lane i holds pair i % 64 of this CTA's 64: keys of the tile's first
         // block of 64 for i < 64, of the second for the others; hs halves both
         // once more.
@@ -849,46 +910,14 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         float* lsum_s = reinterpret_cast<float*>(sgen + kOffLsum);
         float* max_s = reinterpret_cast<float*>(sgen + kOffMax);
         int* bad_s = reinterpret_cast<int*>(sgen + kOffBad);
-        const uint32_t qt0 = mapa(bar(B_QT), 0), sfree0 = mapa(bar(B_SFREE), 0), pfull0 = mapa(bar(B_PFULL), 0);
+        const uint32_t sfree0 = mapa(bar(B_SFREE), 0), pfull0 = mapa(bar(B_PFULL), 0);
         bool ok = true;
-        int ring = 0, rope = 0;   // ring places passed by this unit and those before
         uint32_t own_ph = 0;      // phase of each slot's OWN
         auto own_slot = [&](int place) -> int {
             const int rs = place % kSlots;
             if (!wait_all(bar(B_OWN + rs), (own_ph >> rs) & 1u, abort_flag, 1330 + rs, place)) return -1;
             own_ph ^= 1u << rs;
             return rs;
-        };
-        // Q of the unit at ring place `ring`: columns [0, 384) go to TMEM (row
-        // i % 64 in both lanes), the others to their place in shared memory
-        auto write_q = [&](int units) -> bool {
-            const int s0 = own_slot(ring), s1 = own_slot(ring + 1);
-            if (s0 < 0 || s1 < 0 || !wait_all(bar(B_QROPE), units & 1, abort_flag, 1336, units)) return false;
-            const uint32_t q0 = sbase + kOffRing + s0 * kSlotBytes, q1 = sbase + kOffRing + s1 * kSlotBytes;
-#pragma unroll
-            for (int b = 0; b < 3; ++b) {
-                const int sl = 3 * hs + b;
-                const uint32_t src = (sl < 4 ? q0 + sl * kSlab : q1 + (sl - 4) * kSlab) + lr * 128;
-                uint32_t w[32];
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    const uint4 x = ld_shared_v4(src + ((v ^ (lr & 7)) << 4));
-                    w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
-                }
-                tmem_st32(tmem + lane_addr + kColQ + 32 * sl, w);
-            }
-#pragma unroll
-            for (int it = 0; it < 6; ++it) {
-                const uint32_t o = (uint32_t)(it & 1) * 4096 + threadIdx.x * 16;
-                const uint32_t src = it < 4 ? q1 + (2 + (it >> 1)) * kSlab : sbase + kOffRope + (rope & 1) * kSlab;
-                st_shared_v4(sbase + kOffQ + (it >> 1) * kSlab + o, ld_shared_v4(src + o));
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(qt0);
-            return true;
         };
         // the next part with keys, and what this thread's pair sees
         int np = 0;
@@ -912,8 +941,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         PartInfo u, un;
         Visible vis, vn;
         bool have = advance(u, vis);
-        if (have) ok = write_q(0);
         int g = 0, uc = 0;
+        int ring = -2;            // ring place of the unit's Q (two less for the first: no values before its K(1))
         while (have && ok) {
             const int nt = u.nt;
             bool more = false;
@@ -1010,9 +1039,11 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 for (int m = 0; m < 4; ++m)
                     st_shared_v4(sbase + kOffP + side * kSlab + lr * 128 + (((4 * hs + m) ^ (lr & 7)) << 4),
                                  make_uint4(pk[4 * m], pk[4 * m + 1], pk[4 * m + 2], pk[4 * m + 3]));
+                if (j == 0) more = advance(un, vn);
                 if (!whole) {
-                    // ring places of this tile's values: behind the next tile's keys
-                    const int v0 = ring + 2 + 4 * j + (j < nt - 1 ? 4 : 2);
+                    // ring places of this tile's values: behind the next tile's keys, and
+                    // the next unit's Q before those
+                    const int v0 = ring + 4 * j + (j < nt - 1 ? 8 : more ? 10 : 6);
                     int bad = 0;
 #pragma unroll
                     for (int w = 0; w < 8; ++w) bad |= bad_s[(g & 1) * 8 + w];
@@ -1039,18 +1070,14 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(pfull0);
-                if (j == 0) more = advance(un, vn);     // while the tensor pipe is busy
             }
             ring += 2 + 4 * nt;
-            rope += 1 + nt;
             if (!ok) break;
             // sum and maximum for the warps that take O
             lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
             if (grp == 0) max_s[(uc & 1) * 64 + lr] = m_use;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_LSUM));
-            // every QK of this unit has completed: Q makes room for the next unit's
-            if (more && !write_q(uc + 1)) break;
             u = un;
             vis = vn;
             have = more;
