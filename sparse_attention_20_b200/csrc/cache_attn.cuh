@@ -1,5 +1,5 @@
-// Dense MLA attention (MQA mode) of new tokens over the paged latent cache,
-// and the attention weight each cached token receives from it. Row t of
+// What dense MLA attention (MQA mode) of new tokens over the paged latent cache
+// and the weight each cached token receives from it have in common. Row t of
 // sequence b = seq[t] at position p = pos[t] sees the keys
 //   V(t) = { s <= p },  or with a window W > 0  { s <= p : s > p - W or s < sinks }
 // and
@@ -18,7 +18,6 @@ constexpr int kDv = 512;
 // Visible keys of a row: [lo, hi] and [0, sink_end) (hi = -1: none).
 struct Visible {
     int lo, hi, sink_end;
-    __device__ __forceinline__ bool operator()(int s) const { return s <= hi && (s >= lo || s < sink_end); }
 };
 
 __device__ __forceinline__ Visible visible_of(int n_keys, int pos, int window, int sinks)
