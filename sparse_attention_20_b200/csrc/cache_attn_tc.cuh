@@ -87,12 +87,23 @@ enum : int {
 constexpr int kMaxClusters = 74;
 // A unit's Q, first softmax and epilogue cost about as much as this many tiles.
 constexpr int kUnitCost = 3;
-// Least work of a cluster: below it more clusters only add parts to join.
-constexpr int kMinWork = 8;
+// How many clusters share work `total`: pieces of at least kFullWork, or of
+// kMinWork as long as that is no more than kFewParts clusters (one sequence of
+// 3000 keys: 20.6 us in six pieces, 24.7 in three; of 30000: 36 us in 59, 32 in
+// 32, whose parts the join reads sooner).
+constexpr int kMinWork = 4;
+constexpr int kFullWork = 8;
+constexpr int kFewParts = 32;
+__host__ __device__ __forceinline__ long long pieces_of(long long total, int clusters)
+{
+    const long long few = total / kMinWork < kFewParts ? total / kMinWork : kFewParts;
+    const long long n = total / kFullWork > few ? total / kFullWork : few;
+    return n < 1 ? 1 : n < clusters ? n : clusters;
+}
 // Where there are no more units than clusters and the largest is at most this
-// much above an even piece, each cluster takes a unit whole: a second launch
-// and the parts' way through memory cost some 7 us, the time of six tiles (64
-// windows of 1024 keys: 48 us cut evenly, 33 us whole).
+// much above an even piece (or a full one), each cluster takes a unit whole: a
+// second launch and the parts' way through memory cost some 7 us, the time of
+// six tiles (64 windows of 1024 keys: 48 us cut evenly, 33 us whole).
 constexpr int kWholeSlack = 6;
 
 // A split unit that the cluster of its last tile describes for the join.
@@ -340,7 +351,7 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
         if (w < warp) pre += sums[w];
         p.total += sums[w];
     }
-    p.ncl = max(1, min(clusters, p.total / kMinWork));
+    p.ncl = (int)pieces_of(p.total, clusters);
     p.w0 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid) : p.total;
     p.w1 = cid < p.ncl ? Piece::begin(p.total, p.ncl, cid + 1) : p.total;
     bool mine = p.w0 < p.w1 && sum > 0 && pre <= p.w0 && p.w0 < pre + sum;
@@ -353,7 +364,7 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
             all += units[2 * w];
             largest = max(largest, units[2 * w + 1]);
         }
-        if (all <= clusters && largest <= p.total / p.ncl + kWholeSlack) {
+        if (all <= clusters && largest <= max(p.total / p.ncl, kFullWork) + kWholeSlack) {
             // unit cid, whole; its thread alone knows where it lies
             mine = here > 0 && n_units == cid;
             p.w0 = 0;

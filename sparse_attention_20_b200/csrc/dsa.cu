@@ -1278,13 +1278,13 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     SplitDesc* desc = reinterpret_cast<SplitDesc*>(reinterpret_cast<char*>(workspace) + kPartBytes + kPartLseBytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int most = std::min(kMaxClusters, std::max(1, num_sms() / 2));
-    const int clusters = (int)std::min<long long>(std::max<long long>(work / kMinWork, T), most);
-    // Units of at most kMinWork + kWholeSlack stay whole where each has a cluster:
+    const int clusters = (int)std::max<long long>(pieces_of(work, most), std::min(T, most));
+    // Units of at most kFullWork + kWholeSlack stay whole where each has a cluster:
     // no parts, no join. A unit of one row sees no more tiles than its window.
     long long longest = tiles;
     if (window > 0 && kRows / Hq == 1)
         longest = std::min(longest, ((long long)window + kTile - 1) / kTile + 1 + ((long long)sinks + kTile - 1) / kTile);
-    const bool whole = T <= clusters && longest + kUnitCost <= kMinWork + kWholeSlack;
+    const bool whole = T <= clusters && longest + kUnitCost <= kFullWork + kWholeSlack;
     launch_pdl(mla_attn_paged_tc_kernel, dim3(2 * clusters), dim3(kTcThreads), kTcSmem, st, tm4, tm1, tq4,
                tq1, args, scale * 1.4426950408889634f,
                reinterpret_cast<__nv_bfloat16*>(out), lse, part_o, part_lse, desc);
