@@ -1128,15 +1128,20 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
 {
     __shared__ float wz[kMaxClusters][kJoinRows];
     __shared__ int where[kMaxClusters];
+    __shared__ __align__(16) SplitDesc ds[kMaxClusters];
     __shared__ int active[kMaxClusters];       // clusters that ended a split unit
     __shared__ int n_active;
     griddep_launch();
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    static_assert(sizeof(SplitDesc) == 32, "two 16-byte pieces");
+    for (int i = threadIdx.x; i < 2 * clusters; i += kJoinThreads)
+        reinterpret_cast<uint4*>(ds)[i] = reinterpret_cast<const uint4*>(desc)[i];
+    __syncthreads();
     if (warp == 0) {
         int n = 0;
         for (int c0 = 0; c0 < clusters; c0 += 32) {
-            const bool is = c0 + lane < clusters && desc[c0 + lane].n_rows > 0;
+            const bool is = c0 + lane < clusters && ds[c0 + lane].n_rows > 0;
             const unsigned m = __ballot_sync(0xffffffffu, is);
             if (is) active[n + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
             n += __popc(m);
@@ -1145,10 +1150,26 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
     }
     __syncthreads();
     for (int item = blockIdx.x; item < n_active * kJoinItems; item += gridDim.x) {
-        const SplitDesc d = desc[active[item / kJoinItems]];
+        const SplitDesc d = ds[active[item / kJoinItems]];
         const int e = item % kJoinItems, r0 = e / (kDv / kJoinCols) * kJoinRows, z4 = e % (kDv / kJoinCols);
         if (d.n_rows <= r0) continue;
         const int parts = d.c_last - d.c_first + 1;
+        // a thread per row and two groups of four columns; the first parts' values
+        // are on their way while the weights are found
+        const int rr = threadIdx.x % kJoinRows, c4 = z4 * (kJoinCols / 4) + threadIdx.x / kJoinRows;
+        constexpr int kStep = kJoinThreads / kJoinRows, kFirst = 2;
+        const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)c4 * kRows + min(r0 + rr, d.n_rows - 1);
+        auto slot_of = [&](int z) -> int {
+            const int c = d.c_first + z;
+            return c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
+        };
+        float4 early[kFirst][2];
+#pragma unroll
+        for (int z = 0; z < kFirst; ++z) {
+            const float4* pz = p + (size_t)slot_of(min(z, parts - 1)) * kRows * (kDv / 4);
+            early[z][0] = __ldcs(pz);
+            early[z][1] = __ldcs(pz + (size_t)kStep * kRows);
+        }
         {
             // a warp per row, lanes over the parts
             const int r = r0 + warp;
@@ -1158,8 +1179,7 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
                 const int z = lane + 32 * i;
                 v[i] = -INFINITY;
                 if (z >= parts) continue;
-                const int c = d.c_first + z;
-                const int at = c * 2 + (d.start < Piece::begin(d.total, d.ncl, c) ? 0 : 1);
+                const int at = slot_of(z);
                 if (warp == 0) where[z] = at;
                 if (r < d.n_rows) v[i] = part_lse[at * kRows + r];
                 m = fmaxf(m, v[i]);
@@ -1175,23 +1195,26 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
             if (lane == 0 && z4 == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
         }
         __syncthreads();
-        const int rr = threadIdx.x % kJoinRows, c4 = z4 * (kJoinCols / 4) + threadIdx.x / kJoinRows;
-        constexpr int kStep = kJoinThreads / kJoinRows;
         if (r0 + rr < d.n_rows) {
             float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-            const float4* p = reinterpret_cast<const float4*>(part_o) + (size_t)c4 * kRows + r0 + rr;
+            auto add = [&](float w, float4 v, float4& a) {
+                a.x = fmaf(w, v.x, a.x);
+                a.y = fmaf(w, v.y, a.y);
+                a.z = fmaf(w, v.z, a.z);
+                a.w = fmaf(w, v.w, a.w);
+            };
+#pragma unroll
+            for (int z = 0; z < kFirst; ++z)
+                if (z < parts) {
+                    add(wz[z][rr], early[z][0], acc[0]);
+                    add(wz[z][rr], early[z][1], acc[1]);
+                }
 #pragma unroll 4
-            for (int z = 0; z < parts; ++z) {
+            for (int z = kFirst; z < parts; ++z) {
                 const float w = wz[z][rr];
                 const float4* pz = p + (size_t)where[z] * kRows * (kDv / 4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 v = __ldcs(pz + (size_t)i * kStep * kRows);
-                    acc[i].x = fmaf(w, v.x, acc[i].x);
-                    acc[i].y = fmaf(w, v.y, acc[i].y);
-                    acc[i].z = fmaf(w, v.z, acc[i].z);
-                    acc[i].w = fmaf(w, v.w, acc[i].w);
-                }
+                add(w, __ldcs(pz), acc[0]);
+                add(w, __ldcs(pz + (size_t)kStep * kRows), acc[1]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
