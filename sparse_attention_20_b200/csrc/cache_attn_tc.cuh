@@ -406,21 +406,27 @@ __device__ Piece plan(const Args& a, int cid, int clusters, int* smem, PartInfo*
     return p;
 }
 
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
+// Waits that last as long as a unit (up to 1.5 s of tiles in 180 GB of cache)
+// have this limit; they end with the CTA's abort flag as soon as another gives up.
+constexpr uint64_t kUnitWaitNs = 60ull * 1000000000ull;
+
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c,
+                                         uint64_t limit_ns = kWaitLimitNs)
 {
-    return __all_sync(0xffffffffu, mbar_wait<true>(bar, par, abort_flag, tag, c));
+    return __all_sync(0xffffffffu, mbar_wait<true>(bar, par, abort_flag, tag, c, limit_ns));
 }
 
 // Waits on a barrier per lane, all at once (one round costs about as much as a
 // wait on one barrier). Bounded; the outcome is the warp's.
-__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c)
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t par, volatile int* abort_flag, int tag, int c,
+                                           uint64_t limit_ns = kWaitLimitNs)
 {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, par))) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
         bool mine = mbar_test_wait(bar, par);
         if (__all_sync(0xffffffffu, mine)) return true;
-        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        const bool late = globaltimer_ns() - t0 > limit_ns;
         if (__any_sync(0xffffffffu, late || *abort_flag)) {
             if (late && !mine) report_timeout(tag, c, (int)par);
             *abort_flag = 1;
@@ -739,7 +745,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         while (true) {
             const bool more = pc.w0 < pc.w1 && at < pc.w1 && t < args.T;
             const int slot = np % kAhead;
-            if (!wait_lanes(bar(B_PARTFREE + slot), (uint32_t)(((np / kAhead) & 1) ^ 1), abort_flag, 1060, np)) break;
+            if (!wait_lanes(bar(B_PARTFREE + slot), (uint32_t)(((np / kAhead) & 1) ^ 1), abort_flag, 1060, np,
+                            kUnitWaitNs))
+                break;
             if (!more) {
                 if (el) {
                     infos[slot].nt = -1;
@@ -837,14 +845,14 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             ring += 4 * p.nt + (uc > 0 ? 2 : 0);
             rope += 1 + p.nt;
             if (more) {
-                if (!wait_all(bar(B_QFREE), uc & 1, abort_flag, 1338, uc) || !write_q(uc + 1)) break;
+                if (!wait_all(bar(B_QFREE), uc & 1, abort_flag, 1338, uc, kUnitWaitNs) || !write_q(uc + 1)) break;
             }
             const bool live = r < p.rows;
             const size_t row = (size_t)p.t * args.Hq + r;
             __nv_bfloat16* orow = out + row * kDv + side * 256;
             g += p.nt;
             // row sum over the four threads of the row
-            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g)) break;
+            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g, kUnitWaitNs)) break;
             const float* ls = lsum_s + (uc & 1) * 256 + lr;
             const float l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
             const float m = max_s[(uc & 1) * 64 + lr];
