@@ -382,9 +382,11 @@ def _run(fn, device, stream, *args) -> None:
         raise DSAError(rc, last_error())
 
 
-def _ints(**values) -> None:
+def _ints(window=0, sinks=0, **values) -> None:
     """Sizes that a C int has to hold (ctypes would cut them silently)."""
-    for name, v in values.items():
+    if not values and -0x80000000 <= window < 0x80000000 and -0x80000000 <= sinks < 0x80000000:
+        return
+    for name, v in dict(values, window=window, sinks=sinks).items():
         if not -0x80000000 <= v < 0x80000000:
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
@@ -418,7 +420,7 @@ def _cache_rows(q, kv_pages, page_size, block_table, seq, pos):
         raise TypeError(f"q must be bfloat16 [T, Hq, d_qk], got {q.dtype} {tuple(q.shape)}")
     T, Hq, d_qk = q.shape
     dev = q.device
-    if not (isinstance(kv_pages, torch.Tensor) and kv_pages.dim() == 2 and page_size > 0 and
+    if not (isinstance(kv_pages, torch.Tensor) and kv_pages.dim() == 2 and 0 < page_size < 0x80000000 and
             kv_pages.shape[0] % page_size == 0):
         _pages(kv_pages, "kv_pages", d_qk, torch.bfloat16, page_size, dev)
     rows = kv_pages.shape[0]
@@ -462,17 +464,20 @@ def mla_attn_paged(q, kv_pages, page_size: int, block_table, seq, pos, scale: fl
 
     Buffers not given are allocated on the stream that the call runs on."""
     num_pages, n_seqs, max_pages, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size, block_table, seq, pos)
-    _ints(window=window, sinks=sinks, page_size=page_size)
+    _ints(window, sinks)
     lib = load_library()
     out = _new((T, Hq, d_v), torch.bfloat16, dev, stream) if out is None else \
         _need(out, "out", torch.bfloat16, (T, Hq, d_v), dev)
     lse = _new((T, Hq), torch.float32, dev, stream) if lse is None else \
         _need(lse, "lse", torch.float32, (T, Hq), dev)
     if workspace is None:
-        workspace = _new(_attn_ws_bytes(T, Hq), torch.uint8, dev, stream)
+        nbytes = _attn_ws_bytes(T, Hq)
+        workspace = _new(nbytes, torch.uint8, dev, stream)
+    else:
+        nbytes = _ws(workspace, dev)
     _run(lib.dsa_mla_attn_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages, page_size,
          block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), T, Hq, d_qk, d_v, scale, window,
-         sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
+         sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes)
     return out, lse
 
 
@@ -485,17 +490,20 @@ def mla_attn_mass_paged(q, kv_pages, page_size: int, block_table, seq, pos, lse,
     accumulated into (a new zeroed tensor when None). workspace: see
     ``alloc_mla_mass_workspace``."""
     num_pages, n_seqs, max_pages, T, Hq, d_qk, dev = _cache_rows(q, kv_pages, page_size, block_table, seq, pos)
-    _ints(window=window, sinks=sinks, page_size=page_size)
+    _ints(window, sinks)
     _need(lse, "lse", torch.float32, (T, Hq), dev)
     shape = (n_seqs, max_pages * page_size)
     mass = _new(shape, torch.float32, dev, stream, zero=True) if mass is None else \
         _need(mass, "mass", torch.float32, shape, dev)
     lib = load_library()
     if workspace is None:
-        workspace = _new(_mass_ws_bytes(n_seqs), torch.uint8, dev, stream)
+        nbytes = _mass_ws_bytes(n_seqs)
+        workspace = _new(nbytes, torch.uint8, dev, stream)
+    else:
+        nbytes = _ws(workspace, dev)
     _run(lib.dsa_mla_attn_mass_paged, dev, stream, q.data_ptr(), kv_pages.data_ptr(), num_pages,
          page_size, block_table.data_ptr(), n_seqs, max_pages, seq.data_ptr(), pos.data_ptr(), lse.data_ptr(), T, Hq,
-         d_qk, scale, window, sinks, mass.data_ptr(), workspace.data_ptr(), _ws(workspace, dev))
+         d_qk, scale, window, sinks, mass.data_ptr(), workspace.data_ptr(), nbytes)
     return mass
 
 
