@@ -80,8 +80,8 @@ constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 // each CTA's own.
 enum : int {
     B_FULL = 0, B_EMPTY = 5, B_OWN = 10, B_RFULL = 15, B_REMPTY = 17, B_QT = 19, B_SFULL = 20, B_SFREE = 21,
-    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 27, B_QLOAD = 28,
-    B_OFREE = 30, B_PART = 31, B_PARTFREE = 35, B_QFREE = 39, B_COUNT = 40
+    B_PFULL = 22, B_PVDONE = 23, B_RED = 24, B_LSUM = 26, B_DRAIN = 28, B_QLOAD = 29,
+    B_OFREE = 31, B_PART = 32, B_PARTFREE = 36, B_QFREE = 40, B_COUNT = 41
 };
 
 constexpr int kMaxClusters = 74;
@@ -490,7 +490,10 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         mbar_init(bar(B_QFREE), 1);
         mbar_init(bar(B_SFULL), 1);
         mbar_init(bar(B_PVDONE), 1);
+        // of every other unit each: the softmax may be through the next unit (one of a
+        // single tile) before the O warps have looked for this one's sums
         mbar_init(bar(B_LSUM), 8);
+        mbar_init(bar(B_LSUM + 1), 8);
         mbar_init(bar(B_DRAIN), 1);
         // of every other unit each (a unit's Q may be on its way before the last one's
         // is here): two slots and a rope slot
@@ -852,7 +855,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             __nv_bfloat16* orow = out + row * kDv + side * 256;
             g += p.nt;
             // row sum over the four threads of the row
-            if (!wait_all(bar(B_LSUM), uc & 1, abort_flag, 1340, g, kUnitWaitNs)) break;
+            if (!wait_all(bar(B_LSUM + (uc & 1)), (uc >> 1) & 1, abort_flag, 1340, g, kUnitWaitNs)) break;
             const float* ls = lsum_s + (uc & 1) * 256 + lr;
             const float l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
             const float m = max_s[(uc & 1) * 64 + lr];
@@ -1096,7 +1099,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
             if (grp == 0) max_s[(uc & 1) * 64 + lr] = m_use;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_LSUM));
+            if (lane == 0) mbar_arrive(bar(B_LSUM + (uc & 1)));
             u = un;
             vis = vn;
             have = more;
