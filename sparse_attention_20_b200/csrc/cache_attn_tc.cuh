@@ -545,6 +545,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
         const uint32_t full0 = mapa(bar(B_FULL), 0), rfull0 = mapa(bar(B_RFULL), 0);
         // one box of four slabs (columns 64 * z ..) of 64 rows from `row`; with a
         // barrier of this CTA the warps that wait there look at it before the MMA
+        // (which counts no bytes then; its arrival comes first, so that whatever
+        // follows from the load also follows from the arrival: else the other CTA's
+        // bytes for the slot's next turn could fall into this one)
         auto push = [&](const CUtensorMap* tm, int row, int z, uint32_t own) {
             if (!ok) return;
             ok = wait_lanes(bar(B_EMPTY + slot), ph ^ 1u, abort_flag, 1000 + slot, n);
@@ -552,9 +555,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (el) {
                 const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
                 if (own) {
+                    if (rank == 0) mbar_arrive(bar(B_FULL + slot));
                     mbar_arrive_expect_tx(own, kSlotBytes);
                     tma_load_3d(dst, tm, 0, row, z, own);
-                    if (rank == 0) mbar_arrive(bar(B_FULL + slot));
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + slot), 2 * kSlotBytes);
                     tma_load_3d_pair(dst, tm, 0, row, z, full0 + 8u * (uint32_t)slot);
@@ -574,9 +577,9 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (el) {
                 const uint32_t dst = sbase + kOffRope + rslot * kSlab;
                 if (own) {
+                    if (rank == 0) mbar_arrive(bar(B_RFULL + rslot));
                     mbar_arrive_expect_tx(own, kSlab);
                     tma_load_3d(dst, tm, 0, row, 8, own);
-                    if (rank == 0) mbar_arrive(bar(B_RFULL + rslot));
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_RFULL + rslot), 2 * kSlab);
                     tma_load_3d_pair(dst, tm, 0, row, 8, rfull0 + 8u * (uint32_t)rslot);

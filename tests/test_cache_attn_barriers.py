@@ -35,6 +35,14 @@ def _constants():
     return span, slots, ahead
 
 
+def _full_first(name):
+    """Whether the load of a box with a barrier of its own arrives for the MMA
+    before it announces its bytes."""
+    body = re.search(r"auto " + name + r" = .*?\n        \};", _source(), re.S).group(0)
+    own = body[body.index("if (own)"):body.index("} else {")]
+    return own.index("mbar_arrive(bar(B_") < own.index("mbar_arrive_expect_tx(own")
+
+
 class Graph:
     """Events in program order per role; arrivals and waits of (barrier, phase)."""
 
@@ -123,6 +131,16 @@ def _kernel(parts):
     def in_turn(name, c, n):
         return f"{name}{c}.{n % span['B_' + name]}", n // span["B_" + name]
 
+    full_first = _full_first("push"), _full_first("push_rope")
+
+    def signal(role, c, own, full, first):
+        if own and not first:
+            g.arrive(role, *own)
+        if c == 0 or not own:
+            g.arrive(role, *full)
+        if own and first:
+            g.arrive(role, *own)
+
     # ring places: Q K(0) K(1) V(0) ... V(n-1) as the loads push them
     for c in (0, 1):
         role, place, rope, own_of, cut, keys = f"loads{c}", 0, 0, {}, [], 0
@@ -133,13 +151,9 @@ def _kernel(parts):
             g.wait(role, f"EMPTY{c}.{s}", u - 1)
             g.use(role, f"ring{c}.{s}", u, True)
             if own == "slot":
-                n = own_of.setdefault(s, 0)
+                own = f"OWN{c}.{s}", own_of.setdefault(s, 0)
                 own_of[s] += 1
-                g.arrive(role, f"OWN{c}.{s}", n)
-            elif own:
-                g.arrive(role, *own)
-            if c == 0 or not own:
-                g.arrive(role, f"FULL.{s}", u)
+            signal(role, c, own, (f"FULL.{s}", u), full_first[0])
             place += 1
 
         def push_rope(own):
@@ -147,10 +161,7 @@ def _kernel(parts):
             s, u = rope % 2, rope // 2
             g.wait(role, f"REMPTY{c}.{s}", u - 1)
             g.use(role, f"rope{c}.{s}", u, True)
-            if own:
-                g.arrive(role, *own)
-            if c == 0 or not own:
-                g.arrive(role, f"RFULL.{s}", u)
+            signal(role, c, own, (f"RFULL.{s}", u), full_first[1])
             rope += 1
 
         values = None
@@ -343,6 +354,7 @@ WALKS = {
     "units of one tile": [[T]] * 9,
     "whole tiles, one a unit": [[F]] * 9,
     "one, two and three tiles": [[T], [F, T], [T, F, T], [T], [T], [F, F], [T], [F, F, F, T], [T]],
+    "long units": [[F] * 12 + [T], [F] * 7, [T] + [F] * 9],
     "padding between": [[], [], [T], [], [T], [], [T], [T], [], [F, T], [], [T], []],
     "only padding": [[], []],
     "nothing": [],
