@@ -799,6 +799,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             if (!wait_all(bar(B_QLOAD + (units & 1)), (units >> 1) & 1, abort_flag, 1336, units)) return false;
             const uint32_t q0 = sbase + kOffRing + ring % kSlots * kSlotBytes;
             const uint32_t q1 = sbase + kOffRing + (ring + 1) % kSlots * kSlotBytes;
+            tc_fence_after();     // the MMAs that read the last Q (QFREE) are over
 #pragma unroll 2
             for (int sl = 0; sl < 6; ++sl) {
                 const uint32_t src = (sl < 4 ? q0 + sl * kSlab : q1 + (sl - 4) * kSlab) + lr * 128;

@@ -364,3 +364,12 @@ WALKS = {
 @pytest.mark.parametrize("name", WALKS)
 def test_no_wait_can_miss_its_phase(name):
     assert _kernel(WALKS[name]).check() == []
+
+
+def test_tensor_memory_is_written_behind_a_fence():
+    """The warps that bring Q in overwrite columns that earlier MMAs read: their
+    wait for those MMAs has to be followed by the fence that orders tcgen05
+    accesses behind it."""
+    body = re.search(r"auto write_q = .*?return true;\s*\};", _source(), re.S).group(0)
+    assert "tmem_st32(" in body
+    assert "tc_fence_after();" in body[:body.index("tmem_st32(")]
