@@ -219,8 +219,8 @@ int dsa_cache_evict_select(const float* mass, int max_len, const int32_t* seq_le
  *             of whose pages lies outside the pool, is not moved.
  *   mass      fp32 [n_seqs, max_pages * page_size] or NULL
  * A page may stand in the table once only (a shared prefix has to be copied
- * first). Supported: row bytes multiples of 16 up to 4096. No workspace.
- * Asynchronous on `stream`.
+ * first). Supported: row bytes multiples of 16 up to 4096, max_pages *
+ * page_size and keep <= 2^30. No workspace. Asynchronous on `stream`.
  */
 int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int k_row_bytes, int num_pages,
                             int page_size, const int32_t* block_table, int n_seqs, int max_pages,

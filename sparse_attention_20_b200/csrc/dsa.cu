@@ -1386,8 +1386,12 @@ int dsa_cache_compact_paged(void* kv_pages, int kv_row_bytes, void* k_pages, int
     if (num_pages <= 0 || page_size <= 0 || n_seqs <= 0 || max_pages <= 0 || keep <= 0)
         return fail(DSA_ERR_ARG, "num_pages=%d, page_size=%d, n_seqs=%d, max_pages=%d, keep=%d must be positive",
                     num_pages, page_size, n_seqs, max_pages, keep);
-    if ((long long)num_pages * page_size > INT32_MAX || (long long)max_pages * page_size > INT32_MAX)
+    if ((long long)num_pages * page_size > INT32_MAX)
         return fail(DSA_ERR_UNSUPPORTED, "cache of more than 2^31 rows");
+    // the kernel's 32-bit positions run past the last one by up to a block of its cluster
+    if ((long long)max_pages * page_size > kMaxLen || keep > kMaxLen)
+        return fail(DSA_ERR_UNSUPPORTED, "a table of %lld positions, keep=%d (supported: up to %d)",
+                    (long long)max_pages * page_size, keep, kMaxLen);
     if (kv_row_bytes <= 0 || kv_row_bytes % 16 || kv_row_bytes > kMaxRowBytes ||
         (k_pages && (k_row_bytes <= 0 || k_row_bytes % 16 || k_row_bytes > kMaxRowBytes)))
         return fail(DSA_ERR_UNSUPPORTED, "rows of %d and %d bytes (supported: multiples of 16 up to %d)",
