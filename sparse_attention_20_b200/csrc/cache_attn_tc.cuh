@@ -29,7 +29,11 @@
 // Keys that some rows of a unit do not see: their logits are replaced by
 // -inf whatever the product gave, and where such a key's values hold a NaN or
 // an infinity, 0 times which would reach every row, those are zeroed in
-// shared memory before PV (a row that does see the key has a NaN logit).
+// shared memory before PV. A row that does see the key has a logit of NaN or
+// +inf, and all of its out is NaN, or (infinite columns that its query meets
+// with the opposite sign) one of -inf, and the values' columns that are no
+// numbers are NaN in its out, 0 times them, as in tiles that every row sees:
+// the O warps write those (spread_non_numbers).
 //
 // Warps (16 per CTA): 0-7 softmax (two per TMEM lane quarter, 32 of a row's 64
 // keys each); 8 loads; 9 MMA issue (even CTA); 10 walks the cluster's piece and
@@ -67,7 +71,8 @@ constexpr int kOffLsum = kOffRed + 2 * 4 * 64 * 4;    // [2][4][64] row sums
 constexpr int kOffMax = kOffLsum + 2 * 4 * 64 * 4;    // [2][64] row maxima that the sums refer to
 constexpr int kOffBad = kOffMax + 2 * 64 * 4;         // [2][8] flags of the softmax warps
 constexpr int kAhead = 4;                             // parts handed out ahead
-constexpr int kOffParts = kOffBad + 64;               // [kAhead] PartInfo
+constexpr int kOffLost = kOffBad + 64;                // [2][8] tiles that they leave to spread_non_numbers
+constexpr int kOffParts = kOffLost + 64;              // [kAhead] PartInfo
 constexpr int kOffPlan = kOffParts + kAhead * 64;
 constexpr int kTcSmem = kOffPlan + 384 + 1024;        // + alignment slack
 static_assert(kTcSmem <= 232448, "shared memory");
@@ -122,6 +127,7 @@ constexpr size_t kWsBytes = kPartBytes + kPartLseBytes + kMaxClusters * sizeof(S
 
 struct Args {
     PagedRows pg;
+    const __nv_bfloat16* kv;
     const int* pos;
     int T, Hq, window, sinks;
 };
@@ -448,6 +454,46 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
     if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
     if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
     return w;
+}
+
+// Of a part's nt tiles, tile j stands in this one of 32 groups.
+__device__ __forceinline__ int tile_group(int j, int nt) { return (int)((long long)j * 32 / nt); }
+
+// Pair r of a part: NaN in the columns (256 from 256 * side) in which a key that
+// its row sees holds no number, for the keys whose values PV read as zeros. The
+// row's weight of such a key is 0 or NaN. Rare, so it reads the cache again:
+// the tiles of the groups in `where`. To out (orow), or to its place in the
+// parts (po).
+__device__ __noinline__ void spread_non_numbers(const Args a, const PartInfo p, int r, int side, uint32_t where,
+                                                __nv_bfloat16* orow, float4* po)
+{
+    const int t = p.t + r / a.Hq;
+    Visible v;
+    if (!row_sees(a, a.pg.seq[t], a.pos[t], v)) return;
+#pragma unroll 1
+    for (int j = 0; j < p.nt; ++j) {
+        const int key0 = p.key0(j);
+        if (!((where >> tile_group(j, p.nt)) & 1u) || p.all_see(key0, kTile)) continue;
+#pragma unroll 1
+        for (int s = key0; s < key0 + kTile; ++s) {
+            if (!(seen_bits(v, s) & 1u) || p.all_see(s, 1)) continue;
+            const uint4* c = reinterpret_cast<const uint4*>(a.kv + key_row(a.pg, p.bt, 0, s) * kDqk + side * 256);
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const uint4 w4 = __ldg(c + i);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (((w[e >> 1] >> (16 * (e & 1))) & 0x7F80u) != 0x7F80u) continue;
+                    if (po)
+                        reinterpret_cast<float*>(po + (size_t)(side * 64 + 2 * i + (e >> 2)) * kRows)[e & 3] =
+                            __uint_as_float(0x7FC00000u);
+                    else
+                        orow[8 * i + e] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
+                }
+            }
+        }
+    }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
@@ -865,6 +911,11 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             const float m = max_s[(uc & 1) * 64 + lr];
             const float inv = l != 0.f ? 1.f / l : 0.f;
             const float lv = l != 0.f ? m + __log2f(l) : -INFINITY;
+            // tiles with values that PV read as zeros, of rows that see them
+            const uint32_t* lost8 = reinterpret_cast<const uint32_t*>(sgen + kOffLost) + (uc & 1) * 8;
+            uint32_t where = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) where |= lost8[w];
             if (!wait_all(bar(B_PVDONE), (g - 1) & 1, abort_flag, 1350, g)) break;
             tc_fence_after();
             float4* po = reinterpret_cast<float4*>(part_o) + (size_t)max(p.place, 0) * kRows * (kDv / 4) + r;
@@ -917,6 +968,8 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 else
                     lse[row] = lv * 0.69314718055994531f;
             }
+            if (where && live) spread_non_numbers(args, p, r, side, where, orow, p.place >= 0 ? po : nullptr);
+            __syncwarp();
             p = pn;
             have = more;
             ++uc;
@@ -973,6 +1026,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             const int nt = u.nt;
             bool more = false;
             float m_use = -INFINITY, l = 0.f;
+            uint32_t lost = 0;
             for (int j = 0; j < nt; ++j, ++g) {
                 const int key0 = u.key0(j);
                 const bool whole = u.all_see(key0, kTile);
@@ -1007,6 +1061,13 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                         if (!((bits >> e) & 1u)) x[e] = -INFINITY;
                     }
                     bad = __any_sync(0xffffffffu, bad);
+                    if (bad) {
+                        // a row sees such a key with a logit of -inf
+                        bool low = false;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) low |= ((bits & ~all) >> e & 1u) && x[e] == -INFINITY;
+                        if (__any_sync(0xffffffffu, low)) lost |= 1u << tile_group(j, nt);
+                    }
                     if (lane == 0) bad_s[(g & 1) * 8 + warp] = bad ? 1 : 0;
                 }
                 float mx[16];
@@ -1102,6 +1163,7 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             // sum and maximum for the warps that take O
             lsum_s[((uc & 1) * 4 + grp) * 64 + lr] = l;
             if (grp == 0) max_s[(uc & 1) * 64 + lr] = m_use;
+            if (lane == 0) reinterpret_cast<uint32_t*>(sgen + kOffLost)[(uc & 1) * 8 + warp] = lost;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_LSUM + (uc & 1)));
             u = un;

@@ -1223,11 +1223,12 @@ dsa::PagedRows paged_rows(const int32_t* block_table, const int32_t* seq, int n_
     return pg;
 }
 
-dsa::cache_attn::Args cache_attn_args(const dsa::PagedRows& pg, const int32_t* pos, int T, int Hq, int window,
-                                      int sinks)
+dsa::cache_attn::Args cache_attn_args(const dsa::PagedRows& pg, const void* kv, const int32_t* pos, int T, int Hq,
+                                      int window, int sinks)
 {
     dsa::cache_attn::Args a;
     a.pg = pg;
+    a.kv = reinterpret_cast<const __nv_bfloat16*>(kv);
     a.pos = pos;
     a.T = T;
     a.Hq = Hq;
@@ -1272,7 +1273,7 @@ int dsa_mla_attn_paged(const void* q, const void* kv_pages, int num_pages, int p
     cudaError_t e = cudaFuncSetAttribute(mla_attn_paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kTcSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_attn_paged_tc_kernel)");
-    const Args args = cache_attn_args(pg, pos, T, Hq, window, sinks);
+    const Args args = cache_attn_args(pg, kv_pages, pos, T, Hq, window, sinks);
     float* part_o = reinterpret_cast<float*>(workspace);
     float* part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kPartBytes);
     SplitDesc* desc = reinterpret_cast<SplitDesc*>(reinterpret_cast<char*>(workspace) + kPartBytes + kPartLseBytes);
@@ -1324,7 +1325,7 @@ int dsa_mla_attn_mass_paged(const void* q, const void* kv_pages, int num_pages, 
     if (int rc = make_tmap_slabs(&tq64, q, kSlabs, (uint64_t)T * Hq, 1)) return rc;
     cudaError_t e = cudaFuncSetAttribute(cache_mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cache_mass_tc_kernel)");
-    const Args args = cache_attn_args(pg, pos, T, Hq, window, sinks);
+    const Args args = cache_attn_args(pg, kv_pages, pos, T, Hq, window, sinks);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int clusters = std::min(kMaxClusters, std::max(1, num_sms() / 2));
     if (n_seqs > kNearSeqs) {

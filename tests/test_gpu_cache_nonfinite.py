@@ -1,0 +1,103 @@
+"""Infinities and NaN in cached rows that query rows do see: dense paged
+attention gives what the formulas give, wherever in a tile the key lies."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_20_b200 as dsa
+from sparse_attention_20_b200 import build as dsa_build
+import cache_ref as ref
+from cache_ref import D_V, SCALE
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dsa_build.build()
+    dsa.load_library()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    torch.cuda.synchronize()
+    assert dsa.device_status() == 0
+
+
+def _check(x, window=0, sinks=0):
+    """out and lse against the formulas in 64 bits: the same elements are no
+    numbers, and the others are within cache_ref's bounds, taken over the keys
+    whose rows are finite (others have a weight of 0 where anything is finite)."""
+    out, lse = dsa.mla_attn_paged(*x.args(), SCALE, D_V, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert dsa.device_status() == 0
+    kinds = set()
+    for t in range(x.q.shape[0]):
+        s = ref.seen_keys(x, t, window, sinks)
+        if not len(s):
+            assert bool((out[t] == 0).all()) and bool((lse[t] == -math.inf).all())
+            continue
+        c, q = x.pages[x.rows_of(int(x.seq[t]), s)].double(), x.q[t].double()
+        z = q @ c.T * SCALE
+        l = torch.logsumexp(z, 1)
+        p = torch.exp(z - l[:, None])
+        o = p @ c[:, :D_V]
+        # a logit of +inf: inf - inf in the softmax, hence NaN in lse, too
+        assert torch.equal(torch.isnan(lse[t]), torch.isnan(l) | (l == math.inf)), t
+        assert torch.equal(lse[t] == -math.inf, l == -math.inf), t
+        assert torch.equal(torch.isnan(out[t]), torch.isnan(o)), t
+        assert not bool(torch.isinf(out[t]).any())
+        fin = torch.isfinite(c).all(1)
+        cf, zf = c[fin], z[:, fin]
+        dx = 64 * 2.0 ** -23 * SCALE * (q.abs() @ cf.abs().T).amax(1) + 8 * 2.0 ** -23 * (1 + zf.abs().amax(1)) \
+            if bool(fin.any()) else torch.zeros_like(l)
+        ok = torch.isfinite(l)
+        assert bool(((lse[t].double() - l).abs() <= dx + 4 * 2.0 ** -23 * (1 + l.abs()))[ok].all()), t
+        tol = (2.0 ** -8 + 2 * dx + 2.0 ** -16)[:, None] * (p[:, fin] @ cf[:, :D_V].abs()) + 2.0 ** -8 * o.abs()
+        good = ~torch.isnan(o)
+        assert bool(((out[t].double() - o).abs() <= tol)[good].all()), t
+        kinds |= {"number" if bool(good[h].all()) else "columns" if bool(good[h].any()) else "row"
+                  for h in range(x.q.shape[1])}
+    return kinds
+
+
+def _put(x, b, s, col, value):
+    x.pages[x.rows_of(b, torch.tensor([s], device="cuda")), col] = value
+
+
+@pytest.mark.parametrize("heads,lens,chunk,window,sinks,where", [
+    (128, [300], 3, 0, 0, (298, 299)),            # tiles that only some rows see whole
+    (128, [300], 3, 0, 0, (5, 130)),              # tiles that all do
+    (16, [333, 190], 11, 0, 0, (185, 188, 5)),
+    (16, [333, 190], 11, 70, 5, (3, 124, 130, 187)),
+    (64, [257], 2, 100, 3, (1, 157, 158, 256)),
+    (1, [400], 100, 33, 2, (0, 290, 301, 399)),
+    (128, [20000], 2, 0, 0, (19998, 19999)),      # a unit cut over the clusters
+    (128, [20000], 2, 0, 0, (60, 9000)),
+    (16, [9001], 8, 3000, 5, (2, 5996, 5999, 8998)),
+])
+@pytest.mark.parametrize("col", [7, 300, 570])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_infinite_columns_of_seen_keys(heads, lens, chunk, window, sinks, where, col, value):
+    """Heads whose query has the one sign meet the key with a logit of +inf (all
+    NaN), those of the other with -inf: a weight of 0, and 0 times infinity in
+    that column of out alone (columns from 512 on are not part of out)."""
+    x = ref.make(lens, [chunk] * len(lens), heads, seed=heads + chunk)
+    g = torch.Generator(device="cuda").manual_seed(col)
+    sign = torch.randint(0, 2, (x.q.shape[0], heads), generator=g, device="cuda") * 2 - 1
+    x.q[:, :, col] = (x.q[:, :, col].abs() + 0.25) * sign
+    for b in range(len(lens)):
+        for s in where:
+            _put(x, b, s, col, value)
+    kinds = _check(x, window, sinks)
+    if heads > 1:
+        assert "row" in kinds and ("columns" if col < D_V else "number") in kinds
+
+
+def test_nan_of_seen_keys_and_other_infinities_beside_it():
+    x = ref.make([300, 130], [3, 3], 128, seed=71)
+    _put(x, 0, 299, 3, math.nan)
+    _put(x, 0, 298, 100, math.inf)
+    _put(x, 0, 298, 400, -math.inf)
+    _put(x, 1, 128, 500, math.inf)
+    x.q[:, :, 500] = -x.q[:, :, 500].abs() - 0.25
+    assert _check(x) >= {"row", "columns", "number"}
