@@ -74,6 +74,13 @@ def _put(x, b, s, col, value):
     (128, [20000], 2, 0, 0, (19998, 19999)),      # a unit cut over the clusters
     (128, [20000], 2, 0, 0, (60, 9000)),
     (16, [9001], 8, 3000, 5, (2, 5996, 5999, 8998)),
+    # keys that some rows of a unit see and others do not, alone
+    (16, [333, 190], 11, 0, 0, (185,)),
+    (16, [333, 190], 11, 70, 5, (113, 188)),
+    (64, [257], 2, 100, 3, (156, 256)),
+    (1, [400], 100, 33, 2, (290, 301, 399)),
+    (16, [9001], 8, 3000, 0, (5996, 8998)),
+    (16, [20000], 8, 0, 0, (19995,)),
 ])
 @pytest.mark.parametrize("col", [7, 300, 570])
 @pytest.mark.parametrize("value", [math.inf, -math.inf])
