@@ -158,10 +158,10 @@ int dsa_sparse_mla_attn_paged(const void* q, const void* kv_pages, int num_pages
  * it, whatever the pool holds there (NaN among it). An infinity or NaN in one
  * that it does see reaches it: a logit of NaN or +inf makes the row's lse and
  * out NaN, one of -inf is a weight of 0 (and 0 times a value that is no number
- * is NaN in that column). Consecutive rows of one sequence may be any tokens of
- * it, in any order; those of a chunk are cheapest next to each other.
- * Probabilities are rounded to bf16 for the product with the values; logits,
- * maxima and sums are fp32.
+ * is NaN in that column); where all logits are -inf, lse is -inf and out NaN.
+ * Consecutive rows of one sequence may be any tokens of it, in any order; those
+ * of a chunk are cheapest next to each other. Probabilities are rounded to bf16
+ * for the product with the values; logits, maxima and sums are fp32.
  * Supported: 1 <= Hq <= 128, d_qk = 576, d_v = 512, T * Hq < 2^31, S <= 2^30,
  * T (S / 128 + 4) < 2^31, sinks > 0 only with a window. workspace: dsa_mla_attn_paged_workspace_size(T, Hq)
  * bytes; calls in flight at once, captured graphs among them, need one each.

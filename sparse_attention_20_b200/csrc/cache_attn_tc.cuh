@@ -45,6 +45,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "cache_attn.cuh"
 #include "sm100.cuh"
 
@@ -110,6 +112,9 @@ __host__ __device__ __forceinline__ long long pieces_of(long long total, int clu
 // second launch and the parts' way through memory cost some 7 us, the time of
 // six tiles (64 windows of 1024 keys: 48 us cut evenly, 33 us whole).
 constexpr int kWholeSlack = 6;
+
+// The log2 sum of a part in which a row that sees keys has no logit above -inf.
+constexpr float kAllLowest = -FLT_MAX;
 
 // A split unit that the cluster of its last tile describes for the join.
 struct SplitDesc {
@@ -909,8 +914,20 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
             const float* ls = lsum_s + (uc & 1) * 256 + lr;
             const float l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
             const float m = max_s[(uc & 1) * 64 + lr];
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            const float lv = l != 0.f ? m + __log2f(l) : -INFINITY;
+            float inv = l != 0.f ? 1.f / l : 0.f;
+            float lv = l != 0.f ? m + __log2f(l) : -INFINITY;
+            if (l == 0.f && live) {
+                // no logit above -inf: a row that sees no key gives 0, one that does has no
+                // softmax. For the join such a part's sum is the lowest finite number.
+                const int t = p.t + r / args.Hq;
+                Visible v;
+                if (row_sees(args, args.pg.seq[t], args.pos[t], v) && (v.lo <= v.hi || v.sink_end > 0)) {
+                    if (p.place >= 0)
+                        lv = kAllLowest;
+                    else
+                        inv = __uint_as_float(0x7FC00000u);
+                }
+            }
             // tiles with values that PV read as zeros, of rows that see them
             const uint32_t* lost8 = reinterpret_cast<const uint32_t*>(sgen + kOffLost) + (uc & 1) * 8;
             uint32_t where = 0;
@@ -1265,10 +1282,14 @@ mla_attn_paged_join_kernel(const float* __restrict__ part_o, const float* __rest
             const float ms = m == -INFINITY ? 0.f : m;
             float l = (exp2f(v[0] - ms) + exp2f(v[1] - ms)) + exp2f(v[2] - ms);
             for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            const float total = l != 0.f ? ms + log2f(l) : -INFINITY;
+            // keys seen, and no logit above -inf in any part (nor a NaN): no softmax
+            const bool none = m == kAllLowest && l == l;
+            const float total = l != 0.f && !none ? ms + log2f(l) : -INFINITY;
 #pragma unroll
             for (int i = 0; i < 3; ++i)
-                if (lane + 32 * i < parts) wz[lane + 32 * i][warp] = v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
+                if (lane + 32 * i < parts)
+                    wz[lane + 32 * i][warp] = none ? __uint_as_float(0x7FC00000u)
+                                                   : v[i] == -INFINITY ? 0.f : exp2f(v[i] - total);
             if (lane == 0 && z4 == 0 && r < d.n_rows) lse[(size_t)d.t * Hq + r] = total * 0.69314718055994531f;
         }
         __syncthreads();

@@ -108,3 +108,24 @@ def test_nan_of_seen_keys_and_other_infinities_beside_it():
     _put(x, 1, 128, 500, math.inf)
     x.q[:, :, 500] = -x.q[:, :, 500].abs() - 0.25
     assert _check(x) >= {"row", "columns", "number"}
+
+
+@pytest.mark.parametrize("heads,lens,chunk,window", [(128, [1, 5, 130], 1, 0), (16, [200], 6, 0), (128, [9000], 1, 0),
+                                                     (16, [9000, 40], 3, 0), (16, [300], 6, 20)])
+@pytest.mark.parametrize("col", [100, 575])
+def test_rows_all_of_whose_logits_are_minus_infinity(heads, lens, chunk, window, col):
+    """lse = -inf as the formula has it, and no softmax: out is NaN, unlike that
+    of a row without keys."""
+    x = ref.make(lens, [chunk] * len(lens), heads, seed=72)
+    x.q[:, :, col] = x.q[:, :, col].abs() + 0.25
+    x.q[-1, ::2, col] *= -1                       # these heads: +inf, so lse is NaN, too
+    x.pages[:, col] = -math.inf
+    if x.q.shape[0] > 1:
+        x.seq[0] = -1
+    _check(x, window)
+    # and a single finite key is the whole softmax
+    if window == 0:
+        for b, n in enumerate(lens):
+            _put(x, b, max(0, n - chunk), col, 1.0)
+        x.q[-1, ::2, col] *= -1
+        _check(x)
