@@ -330,27 +330,31 @@ struct StepInfo {
 };
 static_assert(sizeof(StepInfo) == 64, "StepInfo");
 
+// What a look for the next step finds. The waits of the warps that take the steps
+// have a limit, so a walk that passes over many (a sequence with few rows far
+// apart among others', sequences without rows) says so now and then.
+enum : int { kNoMore = 0, kFound = 1, kStillLooking = 2 };
+constexpr int kLookMost = 4096;      // steps and sequences passed over in one go: some 10 ms at most
+
 struct StepWalk {
     long long w0, w1, total, base;
     int ncl, b, tile, q, q1, nq;
-    bool in_tile, any;
+    bool loaded, in_tile, any;
     SeqPlan s;
     Tiles k;
-    __device__ __forceinline__ void load(const Args& a, const Ws& w)
+    // sequence b (false: it has no tiles)
+    __device__ __forceinline__ bool load(const Args& a, const Ws& w)
     {
-        while (b < a.pg.n_seqs) {
-            s = w.seqs[b];
-            k = tiles_of(s.lo, s.hi, a.window > 0 ? a.sinks : 0);
-            nq = steps_of(s, a.Hq);
-            if (k.nt > 0) return;
-            ++b;
-        }
+        s = w.seqs[b];
+        k = tiles_of(s.lo, s.hi, a.window > 0 ? a.sinks : 0);
+        nq = steps_of(s, a.Hq);
+        return k.nt > 0;
     }
     __device__ __forceinline__ StepWalk(const Args& a, const Ws& w, int cid)
     {
         total = w.head->total;
         ncl = w.head->ncl;
-        in_tile = any = false;
+        loaded = in_tile = any = false;
         b = a.pg.n_seqs;
         w0 = w1 = base = 0;
         tile = q = q1 = nq = 0;
@@ -358,13 +362,22 @@ struct StepWalk {
         w0 = piece_begin(total, ncl, cid);
         w1 = piece_begin(total, ncl, cid + 1);
         b = w.head->first[cid];
-        load(a, w);
+        loaded = load(a, w);      // a cluster's first sequence has tiles
         tile = (int)((w0 - s.start) / (nq + kTileCost));
         base = s.start + (long long)tile * (nq + kTileCost);
     }
-    __device__ __forceinline__ bool next(const Args& a, const Ws& w, Step& st)
+    __device__ __forceinline__ int next(const Args& a, const Ws& w, Step& st)
     {
+        int passed = 0;
         while (b < a.pg.n_seqs && base < w1) {
+            if (!loaded) {
+                loaded = load(a, w);
+                if (!loaded) {
+                    ++b;
+                    if (++passed == kLookMost) return kStillLooking;
+                    continue;
+                }
+            }
             const long long d = base + kTileCost;
             if (!in_tile) {
                 q = (int)max(0ll, min((long long)nq, w0 - d));
@@ -389,8 +402,9 @@ struct StepWalk {
                 ++q;
                 if (st.key0 <= st.rg.hi && (st.key0 + kTile > st.rg.lo || st.key0 < sink_end)) {
                     any = true;
-                    return true;
+                    return kFound;
                 }
+                if (++passed == kLookMost) return kStillLooking;
             }
             // the tile's share is over
             in_tile = false;
@@ -399,16 +413,20 @@ struct StepWalk {
             if (++tile == k.nt) {
                 ++b;
                 tile = 0;
-                load(a, w);
+                loaded = false;
             }
             if (due) {
                 st.n = 0;
-                return true;
+                return kFound;
             }
         }
-        return false;
+        return kNoMore;
     }
 };
+
+// Limit of the waits that the other CTA's share of a step is part of: each CTA
+// walks for itself, so after a long look they may be seconds apart.
+constexpr uint64_t kApartNs = cache_attn::kUnitWaitNs;
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q128,
@@ -476,7 +494,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
     // step gd for the loads' and the issuing warp, which need nothing more of it
     auto take_step = [&](int gd, StepInfo& st) -> bool {
         const int at = gd % kAhead;
-        if (!wait_lanes(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2050, gd)) return false;
+        if (!wait_lanes(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2050, gd, kApartNs)) return false;
         st = reinterpret_cast<const StepInfo*>(sgen + kOffStep)[at];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_STEPFREE + at));
@@ -506,7 +524,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 // a fresh tile waits for its slab of keys, too
                 const bool two = fresh && lane == 1;
                 ok = wait_lanes(two ? bar(B_KEMPTY + k) : bar(B_QEMPTY + slot), two ? (uint32_t)((n_tiles & 1) ^ 1) : ph ^ 1u,
-                                abort_flag, 2000 + k, n_tiles);
+                                abort_flag, 2000 + k, n_tiles, kApartNs);
                 if (!ok) break;
                 if (el) {
                     if (fresh) {
@@ -559,7 +577,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                     wb = bar(B_DFREE + (g & 1));
                     wp = (uint32_t)(((g - 2) >> 1) & 1);
                 }
-                ok = wait_lanes(wb, wp, abort_flag, 2100 + k, g);
+                ok = wait_lanes(wb, wp, abort_flag, 2100 + k, g, kApartNs);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ak = d_k + (uint64_t)(k * (kKSlab >> 4)), bq = d_q + (uint64_t)(slot * (kQSlot >> 4));
@@ -587,22 +605,38 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         int gd = 0, b_prev = -1, tile_prev = -1, row0 = 0, row1 = 0;
         bool ok = true;
         StepWalk walk(args, ws, cid);
+        // the place of step gd
+        auto room = [&]() -> bool {
+            return ok = wait_lanes(bar(B_STEPFREE + gd % kAhead), (uint32_t)(((gd / kAhead) & 1) ^ 1), abort_flag,
+                                   2300, gd, kApartNs);
+        };
+        // the next step of the walk; steps without work meanwhile, where it takes long
+        auto look = [&](Step& s) -> bool {
+            while (true) {
+                const int found = walk.next(args, ws, s);
+                if (found != kStillLooking) return found == kFound;
+                if (el) {
+                    StepInfo none = {};
+                    none.part = -1;
+                    info[gd % kAhead] = none;
+                    mbar_arrive(bar(B_STEP + gd % kAhead));
+                }
+                __syncwarp();
+                ++gd;
+                if (!room()) return false;
+            }
+        };
         Step cur, nxt;
-        bool have = walk.next(args, ws, cur);
+        room();
+        bool have = look(cur);
         while (ok) {
-            const int buf = gd % kAhead;
-            ok = wait_lanes(bar(B_STEPFREE + buf), (uint32_t)(((gd / kAhead) & 1) ^ 1), abort_flag, 2300, gd);
-            if (!ok) break;
             if (!have) {
                 if (el) {
-                    info[buf].N = -1;
-                    mbar_arrive(bar(B_STEP + buf));
+                    info[gd % kAhead].N = -1;
+                    mbar_arrive(bar(B_STEP + gd % kAhead));
                 }
                 break;
             }
-            float* cl = col_f + buf * 3 * kPairs;
-            int* ch = reinterpret_cast<int*>(cl + kPairs);
-            int* co = ch + kPairs;
             const int N = cur.n > 0 ? n_of(cur) : 0, cols = cur.n * args.Hq;
             // a column's lse and the keys that its row sees (none: a column without a
             // row of this sequence, or with nothing to give)
@@ -626,7 +660,12 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             Visible mine;
             bool live = false;
             if (lane < cur.n) live = sees(args, cur.b, cur.t0 + lane, mine);
-            const bool more = walk.next(args, ws, nxt);
+            const bool more = look(nxt);
+            if (!ok) break;
+            const int buf = gd % kAhead;
+            float* cl = col_f + buf * 3 * kPairs;
+            int* ch = reinterpret_cast<int*>(cl + kPairs);
+            int* co = ch + kPairs;
             bool used = true;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -686,6 +725,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
             cur = nxt;
             have = more;
             ++gd;
+            room();
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------- sums
@@ -704,7 +744,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
         float sum = 0.f;
         for (int gd = 0;; ++gd) {
             const int at = gd % kAhead;
-            if (!wait_all(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2200, gd)) break;
+            if (!wait_all(bar(B_STEP + at), (gd / kAhead) & 1, abort_flag, 2200, gd, kApartNs)) break;
             const StepInfo st = info[at];
             if (st.N < 0) break;
             const int key = st.key0 + 128 * (int)rank + i;
@@ -713,7 +753,7 @@ cache_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_con
                 const int* ch = reinterpret_cast<const int*>(cl + kPairs);
                 const int* co = ch + kPairs;
                 const int buf = g & 1;
-                if (!wait_all(bar(B_DFULL + buf), (g >> 1) & 1, abort_flag, 2210, g)) break;
+                if (!wait_all(bar(B_DFULL + buf), (g >> 1) & 1, abort_flag, 2210, g, kApartNs)) break;
                 tc_fence_after();
                 const int per = st.N / 2;
                 const uint32_t ta = tmem + lane_addr + (uint32_t)buf * 256 + hs * per;
