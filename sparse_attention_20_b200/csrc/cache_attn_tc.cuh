@@ -62,8 +62,7 @@ constexpr int kPlanWarps = kTcThreads / 32;
 constexpr int kSlab = 64 * 128;            // 64 rows x 64 columns bf16, 128B swizzle
 constexpr int kSlotBytes = 4 * kSlab;
 constexpr int kSlots = 5;
-constexpr int kQSlabsTmem = 6;             // columns [0, 384) of Q in TMEM, the rest in shared memory
-constexpr int kOffQ = 0;
+constexpr int kOffQ = 0;                   // columns [384, 576) of Q; the others are in TMEM
 constexpr int kOffP = kOffQ + 3 * kSlab;
 constexpr int kOffRope = kOffP + 2 * kSlab;
 constexpr int kOffRing = kOffRope + 2 * kSlab;
@@ -1107,8 +1106,10 @@ mla_attn_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_kv4, const __gri
                 const float f = rescale ? ex2(m_use - m_new) : 1.f;
                 if (raise) m_use = m_new;
                 const float msub = m_use == -INFINITY ? 0.f : m_use;
-                // P goes to the MMA in bf16 (half a step is 2^-9 of each weight, below
-                // the output's own rounding); its sum is taken before, in fp32
+                // P goes to the MMA in bf16, the type of the values that it meets there: at
+                // most half a step, 2^-8 of each weight, like the output's own rounding, and
+                // less in a sum over many keys (relative error of out 0.0017 to 0.0022 against
+                // 64 bits, 0.0017 of it the output's); its sum is taken before, in fp32
                 uint32_t pk[16];
                 float ps[16];
 #pragma unroll

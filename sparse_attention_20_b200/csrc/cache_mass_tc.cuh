@@ -277,7 +277,6 @@ __device__ __forceinline__ bool sees(const Args& a, int b, int t, Visible& v)
 // those of them that belong to b see.
 struct StepRange {
     int hi, min_hi, lo, max_lo;
-    bool all;            // every one belongs to b and sees a key
 };
 
 __device__ __forceinline__ StepRange step_range(const Args& a, int b, int t0, int n)
@@ -286,7 +285,6 @@ __device__ __forceinline__ StepRange step_range(const Args& a, int b, int t0, in
     r.hi = -1;
     r.min_hi = r.lo = INT_MAX;
     r.max_lo = 0;
-    bool all = true;
     for (int i = threadIdx.x & 31; i < n; i += 32) {
         Visible v;
         if (sees(a, b, t0 + i, v)) {
@@ -294,15 +292,12 @@ __device__ __forceinline__ StepRange step_range(const Args& a, int b, int t0, in
             r.min_hi = min(r.min_hi, v.hi);
             r.lo = min(r.lo, v.lo);
             r.max_lo = max(r.max_lo, v.lo);
-        } else {
-            all = false;
         }
     }
     r.hi = __reduce_max_sync(0xffffffffu, r.hi);
     r.min_hi = __reduce_min_sync(0xffffffffu, r.min_hi);
     r.lo = __reduce_min_sync(0xffffffffu, r.lo);
     r.max_lo = __reduce_max_sync(0xffffffffu, r.max_lo);
-    r.all = __all_sync(0xffffffffu, all);
     return r;
 }
 
