@@ -129,3 +129,39 @@ def test_rows_all_of_whose_logits_are_minus_infinity(heads, lens, chunk, window,
             _put(x, b, max(0, n - chunk), col, 1.0)
         x.q[-1, ::2, col] *= -1
         _check(x)
+
+
+@pytest.mark.parametrize("heads,chunk,window,sinks", [(128, 2, 0, 0), (16, 7, 0, 0), (16, 7, 60, 3)])
+def test_received_weights_beside_infinite_keys(heads, chunk, window, sinks):
+    """A key that is met with a logit of -inf receives nothing, and the others
+    what they would without it; a logit of +inf makes a row's weights NaN, on
+    the keys that it sees alone."""
+    x = ref.make([333, 190], [chunk, chunk], heads, seed=73)
+    x.q[:, :, 9] = -x.q[:, :, 9].abs() - 0.25
+    inf_keys = [(0, 331), (0, 290), (1, 188), (1, 1)]
+    for b, s in inf_keys:
+        _put(x, b, s, 9, math.inf)
+    _, lse = dsa.mla_attn_paged(*x.args(), SCALE, D_V, window=window, sinks=sinks)
+    start = torch.rand(2, x.S, device="cuda")
+    mass = dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, mass=start.clone(), window=window, sinks=sinks)
+    # cache_ref.received, its bound taken over the keys whose rows are finite
+    want, adds, rel = start.double(), torch.zeros(2, x.S, dtype=torch.float64, device="cuda"), 0.0
+    for t in range(x.q.shape[0]):
+        b, k = int(x.seq[t]), ref.seen_keys(x, t, window, sinks)
+        c, q, l = x.pages[x.rows_of(b, k)].double(), x.q[t].double(), lse[t].double()
+        z = q @ c.T * SCALE
+        want[b, k] += torch.exp(z - l[:, None]).sum(0)
+        adds[b, k] += heads
+        fin = torch.isfinite(c).all(1)
+        big = z[:, fin].abs().max() + l.abs().max()
+        rel = max(rel, float(64 * 2.0 ** -23 * SCALE * (q.abs() @ c[fin].abs().T).max() + 8 * 2.0 ** -23 * (1 + big)))
+    assert bool(((mass.double() - want).abs() <= want * (rel + (adds + 1) * 2.0 ** -24)).all())
+    for b, s in inf_keys:
+        assert float(mass[b, s]) == float(start[b, s])
+    # one head of the last row meets one of them with +inf
+    x.q[-1, 0, 9] *= -1
+    _, lse = dsa.mla_attn_paged(*x.args(), SCALE, D_V, window=window, sinks=sinks)
+    mass = dsa.mla_attn_mass_paged(*x.args(), lse, SCALE, mass=start.clone(), window=window, sinks=sinks)
+    seen = torch.zeros(2, x.S, dtype=torch.bool, device="cuda")
+    seen[1, ref.seen_keys(x, x.q.shape[0] - 1, window, sinks)] = True
+    assert bool(torch.isnan(lse[-1, 0])) and torch.equal(torch.isnan(mass), seen)
